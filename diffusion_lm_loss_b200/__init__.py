@@ -11,7 +11,8 @@ Two layers:
     ``dlm_loss_fwd_bwd``, ``dlm_linear_loss_fwd_bwd``, ...);
   * tensor helpers with the same names minus the prefix (``sample_t``,
     ``corrupt``, ``loss_fwd_bwd``, ``linear_loss_fwd_bwd``,
-    ``linear_loss_uniform_fwd_bwd``, ``decision_loss_fwd_bwd``) that check every tensor argument's
+    ``linear_loss_uniform_fwd_bwd``, ``decision_loss_fwd_bwd``, and next to the losses ``embed_fwd`` /
+    ``embed_bwd``, ``norm_fwd`` / ``norm_bwd``, ``pack8`` / ``unpack8``) that check every tensor argument's
     dtype, size against the layout and device, allocate outputs and
     workspace with torch on the current device and call the ABI on the
     current torch stream;
@@ -20,7 +21,9 @@ Two layers:
     ``linear_uniform_loss``, ``decision_loss``): the forward runs the fused
     forward + backward call and keeps its gradients; the backward hands them
     over, multiplied by the upstream gradient in the library
-    (``dlm_scale_bf16``, which does nothing when that gradient is 1).
+    (``dlm_scale_bf16``, which does nothing when that gradient is 1); and of
+    the embedding and the norm (``embed``, ``norm``, the norm's input kept in
+    8 bits until its backward pass on request).
 """
 from __future__ import annotations
 
@@ -49,6 +52,12 @@ LABEL_SOFTMAX_RESTRICTED, LABEL_SOFTMAX_FULL, LABEL_SOFTMAX_BOTH = 1, 2, 3
 DECISION_MAX_ANSWERS = 128
 DECISION_MAX_SLOTS = 65535
 
+NORM_LAYER, NORM_RMS = 0, 1
+PACK_NONE, PACK_INT8, PACK_E4M3 = 0, 1, 2
+PACK_BLOCK = 128
+# types of parameters and of their gradients (DLM_BF16, DLM_F32)
+PARAM_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
 STATUS = {0: "DLM_OK", 1: "DLM_ERR_INVALID_ARGUMENT", 2: "DLM_ERR_UNSUPPORTED",
           3: "DLM_ERR_WORKSPACE_TOO_SMALL", 4: "DLM_ERR_CUDA"}
 
@@ -59,7 +68,8 @@ EXPORTS = ("dlm_status_string", "dlm_last_cuda_error", "dlm_version", "dlm_sampl
            "dlm_linear_loss_fwd_bwd", "dlm_linear_loss_fwd_bwd_ex", "dlm_linear_loss_uniform_workspace_size",
            "dlm_linear_loss_uniform_fwd_bwd", "dlm_decision_workspace_size", "dlm_decision_loss_fwd_bwd",
            "dlm_scale_bf16", "dlm_get_device_status", "dlm_selftest_bounded_wait",
-           "dlm_test_skip_device_check")
+           "dlm_test_skip_device_check", "dlm_embed_fwd", "dlm_embed_bwd_workspace_size", "dlm_embed_bwd",
+           "dlm_norm_fwd", "dlm_norm_bwd_workspace_size", "dlm_norm_bwd", "dlm_pack8", "dlm_unpack8")
 
 
 class DlmError(RuntimeError):
@@ -174,6 +184,23 @@ def lib():
     L.dlm_test_skip_device_check.argtypes = [i32]
     L.dlm_selftest_bounded_wait.restype = ctypes.c_int
     L.dlm_selftest_bounded_wait.argtypes = [u64, vp, vp]
+    L.dlm_embed_fwd.restype = ctypes.c_int
+    L.dlm_embed_fwd.argtypes = [lp, vp, vp, i64, i32, i32, f32, vp, i64, vp, vp]
+    L.dlm_embed_bwd_workspace_size.restype = sz
+    L.dlm_embed_bwd_workspace_size.argtypes = [lp, i32, i32]
+    L.dlm_embed_bwd.restype = ctypes.c_int
+    L.dlm_embed_bwd.argtypes = [lp, vp, vp, i64, i32, i32, f32, i32, i32, vp, i64, vp, sz, vp]
+    L.dlm_norm_fwd.restype = ctypes.c_int
+    L.dlm_norm_fwd.argtypes = [vp, i64, i32, i64, vp, vp, i32, i32, f32, f32, vp, i64, vp, vp, i32, vp, vp, vp]
+    L.dlm_norm_bwd_workspace_size.restype = sz
+    L.dlm_norm_bwd_workspace_size.argtypes = [i64, i32]
+    L.dlm_norm_bwd.restype = ctypes.c_int
+    L.dlm_norm_bwd.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, i32, i32, f32, i64, i32, vp, i64, i32, i32,
+                               vp, vp, vp, sz, vp]
+    L.dlm_pack8.restype = ctypes.c_int
+    L.dlm_pack8.argtypes = [vp, i64, i32, i64, i32, vp, vp, vp]
+    L.dlm_unpack8.restype = ctypes.c_int
+    L.dlm_unpack8.argtypes = [vp, vp, i64, i32, i32, vp, i64, vp]
     L.dlm_get_device_status.restype = ctypes.c_int
     L.dlm_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
     _lib = L
@@ -572,6 +599,310 @@ def device_status(workspace: torch.Tensor) -> int:
 
 
 # --------------------------------------------------------------------------
+# embedding, norm, activations in 8 bits
+# --------------------------------------------------------------------------
+def _call(dev: torch.device, name: str, *args):
+    """A library call on the current stream of `dev`, which becomes the
+    current device for it."""
+    fn = getattr(lib(), name)
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _ok(fn(*args, _stream()), name)
+    else:
+        _ok(fn(*args, _stream()), name)
+
+
+def _check_rows(t: Optional[torch.Tensor], dtype, name: str, rows: int, cols: int) -> int:
+    """A [rows, cols] argument with unit column stride (`rows`: at least so
+    many); its row stride."""
+    _check(t, dtype, name, min_rows=rows)
+    if t.shape[1] != cols:
+        raise ValueError(f"{name}: must have {cols} columns, has {t.shape[1]}")
+    ld = t.stride(0) if t.shape[0] > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap (row stride {ld}, {cols} columns)")
+    return ld
+
+
+def _as_rows(t: torch.Tensor) -> torch.Tensor:
+    """An upstream gradient [rows, cols] as _check_rows wants it (an expanded
+    or transposed one is copied)."""
+    ok = t.shape[1] <= 1 or t.stride(1) == 1
+    return t if ok and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]) else t.contiguous()
+
+
+def _param_dtype(dtype, name: str) -> int:
+    if dtype not in PARAM_DTYPES:
+        raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {dtype}")
+    return PARAM_DTYPES[dtype]
+
+
+def embed_fwd(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
+              out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """scale * weight[ids] as bf16 [n_tokens, d_model] (see dlm_embed_fwd);
+    rows of pads are zeros.  dev_status: an int32 / uint32 tensor that gets
+    DEV_BAD_TOKEN_ID or'ed in when an id is outside the table."""
+    T = layout.n_tokens
+    _check(ids, torch.int32, "ids", min_numel=T)
+    _check(weight, torch.bfloat16, "weight")
+    if weight.dim() != 2 or weight.shape[0] < 1 or weight.shape[1] < 1:
+        raise ValueError("weight: [vocab, d_model]")
+    V, D = weight.shape
+    ld_w = _check_rows(weight, torch.bfloat16, "weight", V, D)
+    if dev_status is not None and (dev_status.dtype not in (torch.int32, torch.uint32) or dev_status.numel() < 1):
+        raise ValueError("dev_status: an int32 / uint32 tensor of at least one element")
+    ld_out = D if out is None else _check_rows(out, torch.bfloat16, "out", T, D)
+    _on_cuda(ids=ids, weight=weight, out=out, dev_status=dev_status)
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.bfloat16, device=weight.device)
+    _call(weight.device, "dlm_embed_fwd", ctypes.byref(layout), _ptr(ids), _ptr(weight), ld_w, V, D, scale, _ptr(out),
+          ld_out, _ptr(dev_status))
+    return out
+
+
+@dataclass
+class EmbedGrad:
+    d_weight: torch.Tensor        # bf16 or float32 [vocab, d_model]
+    workspace: torch.Tensor       # uint8; holds the device status word
+
+    def device_status(self) -> int:
+        return device_status(self.workspace)
+
+
+def embed_bwd_workspace_size(layout: Layout, d_model: int, vocab: int) -> int:
+    return int(lib().dlm_embed_bwd_workspace_size(ctypes.byref(layout), d_model, vocab))
+
+
+def embed_bwd(layout: Layout, ids: torch.Tensor, d_out: torch.Tensor, vocab: int, scale: float = 1.0,
+              grad_dtype: torch.dtype = torch.bfloat16, d_weight: Optional[torch.Tensor] = None,
+              accumulate: bool = False, workspace: Optional[torch.Tensor] = None) -> EmbedGrad:
+    """Gradient of embed_fwd's table (see dlm_embed_bwd), in a new tensor of
+    grad_dtype or in `d_weight` (whose type then counts).  accumulate: added to
+    what d_weight holds, e.g. the d_weight of a tied output head."""
+    T = layout.n_tokens
+    _check(ids, torch.int32, "ids", min_numel=T)
+    _check(d_out, torch.bfloat16, "d_out", min_rows=T)
+    D = d_out.shape[1]
+    if D < 1 or vocab < 1:
+        raise ValueError("d_out and the table need at least one column and one row")
+    ld = _check_rows(d_out, torch.bfloat16, "d_out", T, D)
+    if accumulate and d_weight is None:
+        raise ValueError("accumulate needs d_weight")
+    if d_weight is not None:
+        grad_dtype = d_weight.dtype
+    gt = _param_dtype(grad_dtype, "grad_dtype" if d_weight is None else "d_weight")
+    ld_dw = D if d_weight is None else _check_rows(d_weight, grad_dtype, "d_weight", vocab, D)
+    if workspace is not None:
+        _check(workspace, torch.uint8, "workspace", min_numel=0)
+    _on_cuda(ids=ids, d_out=d_out, d_weight=d_weight, workspace=workspace)
+    dev = d_out.device
+    if d_weight is None:
+        d_weight = torch.empty((vocab, D), dtype=grad_dtype, device=dev)
+    if workspace is None:
+        workspace = _aligned_workspace(embed_bwd_workspace_size(layout, D, vocab), dev, 256)
+    _call(dev, "dlm_embed_bwd", ctypes.byref(layout), _ptr(ids), _ptr(d_out), ld, vocab, D, scale, gt, int(accumulate),
+          _ptr(d_weight), ld_dw, _ptr(workspace), workspace.numel())
+    return EmbedGrad(d_weight, workspace)
+
+
+@dataclass
+class Packed8:
+    """An activation [rows, cols] in 8 bits (see dlm_pack8)."""
+    q: torch.Tensor               # uint8 [rows, cols]: the codes' bytes
+    scale: torch.Tensor           # float32 [rows, ceil(cols / PACK_BLOCK)]
+    format: int                   # PACK_INT8 | PACK_E4M3
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+
+def _empty_packed(rows: int, cols: int, fmt: int, dev) -> Packed8:
+    return Packed8(torch.empty((rows, cols), dtype=torch.uint8, device=dev),
+                   torch.empty((rows, -(-cols // PACK_BLOCK)), dtype=torch.float32, device=dev), fmt)
+
+
+def _check_packed(p: Packed8, rows: int, cols: int, name: str):
+    if p.format not in (PACK_INT8, PACK_E4M3):
+        raise ValueError(f"{name}: format must be PACK_INT8 or PACK_E4M3")
+    _check(p.q, torch.uint8, f"{name}.q", min_numel=0)
+    _check(p.scale, torch.float32, f"{name}.scale", min_numel=0)
+    if tuple(p.q.shape) != (rows, cols) or tuple(p.scale.shape) != (rows, -(-cols // PACK_BLOCK)):
+        raise ValueError(f"{name}: q [{rows}, {cols}] and scale [{rows}, {-(-cols // PACK_BLOCK)}], got "
+                         f"{tuple(p.q.shape)} and {tuple(p.scale.shape)}")
+
+
+def pack8(x: torch.Tensor, format: int = PACK_INT8, out: Optional[Packed8] = None) -> Packed8:
+    """x (bf16 [rows, cols]) in 8 bits, one float factor per PACK_BLOCK
+    columns (see dlm_pack8)."""
+    _check(x, torch.bfloat16, "x", min_rows=0)
+    rows, cols = x.shape
+    ld = _check_rows(x, torch.bfloat16, "x", rows, cols)
+    if out is not None:
+        _check_packed(out, rows, cols, "out")
+        if out.format != format:
+            raise ValueError("out: has another format")
+    elif format not in (PACK_INT8, PACK_E4M3):
+        raise ValueError("format: PACK_INT8 or PACK_E4M3")
+    _on_cuda(x=x, q=out.q if out is not None else None, scale=out.scale if out is not None else None)
+    if out is None:
+        out = _empty_packed(rows, cols, format, x.device)
+    _call(x.device, "dlm_pack8", _ptr(x), rows, cols, ld, format, _ptr(out.q), _ptr(out.scale))
+    return out
+
+
+def unpack8(packed: Packed8, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The bf16 values that pack8's (or norm_fwd's) codes stand for."""
+    _check(packed.q, torch.uint8, "packed.q", min_rows=0)
+    rows, cols = packed.q.shape
+    _check_packed(packed, rows, cols, "packed")
+    ld = cols if out is None else _check_rows(out, torch.bfloat16, "out", rows, cols)
+    _on_cuda(q=packed.q, scale=packed.scale, out=out)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=packed.q.device)
+    _call(packed.q.device, "dlm_unpack8", _ptr(packed.q), _ptr(packed.scale), rows, cols, packed.format, _ptr(out), ld)
+    return out
+
+
+@dataclass
+class NormOut:
+    y: torch.Tensor               # bf16 [rows, d_model]
+    mean: Optional[torch.Tensor]  # float32 [rows] (None: RMS)
+    rstd: torch.Tensor            # float32 [rows]
+    packed: Optional[Packed8]     # x in 8 bits, when asked for
+
+
+def _check_params(weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], cols: int) -> int:
+    """weight and bias [cols] of one type; its DLM_* number."""
+    dtype = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        dt = _param_dtype(t.dtype, name)
+        _check(t, t.dtype, name, min_numel=cols)
+        if t.dim() != 1 or t.numel() != cols:
+            raise ValueError(f"{name}: must have shape ({cols},), has {tuple(t.shape)}")
+        if dtype is not None and dt != dtype:
+            raise TypeError("weight and bias: must have one type")
+        dtype = dt
+    return 0 if dtype is None else dtype
+
+
+def norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+             eps: float = 1e-5, kind: int = NORM_LAYER, weight_offset: float = 0.0, pack: int = PACK_NONE,
+             out: Optional[NormOut] = None) -> NormOut:
+    """Layer norm or RMS norm of the rows of x (bf16 [rows, d_model]; see
+    dlm_norm_fwd).  pack: also x in 8 bits, which norm_bwd takes in x's place.
+    Reuses the buffers of `out` when given."""
+    _check(x, torch.bfloat16, "x", min_rows=0)
+    rows, D = x.shape
+    ld = _check_rows(x, torch.bfloat16, "x", rows, D)
+    pt = _check_params(weight, bias, D)
+    if pack not in (PACK_NONE, PACK_INT8, PACK_E4M3):
+        raise ValueError("pack: PACK_NONE, PACK_INT8 or PACK_E4M3")
+    layer = kind == NORM_LAYER
+    ld_y, pk = D, None
+    if out is not None:
+        ld_y = _check_rows(out.y, torch.bfloat16, "out.y", rows, D)
+        if layer:
+            _check(out.mean, torch.float32, "out.mean", min_numel=rows)
+        _check(out.rstd, torch.float32, "out.rstd", min_numel=rows)
+        if pack != PACK_NONE:
+            if out.packed is None or out.packed.format != pack:
+                raise ValueError("out.packed: required, in the format asked for")
+            pk = out.packed
+            _check_packed(pk, rows, D, "out.packed")
+        _on_cuda(x=x, weight=weight, bias=bias, y=out.y, mean=out.mean if layer else None, rstd=out.rstd,
+                 q=pk.q if pk is not None else None, scale=pk.scale if pk is not None else None)
+    else:
+        _on_cuda(x=x, weight=weight, bias=bias)
+        dev = x.device
+        stats = torch.empty((2 if layer else 1, rows), dtype=torch.float32, device=dev)
+        pk = _empty_packed(rows, D, pack, dev) if pack != PACK_NONE else None
+        out = NormOut(torch.empty((rows, D), dtype=torch.bfloat16, device=dev), stats[1] if layer else None, stats[0],
+                      pk)
+    _call(x.device, "dlm_norm_fwd", _ptr(x), rows, D, ld, _ptr(weight), _ptr(bias), pt, kind, eps, weight_offset,
+          _ptr(out.y), ld_y, _ptr(out.mean) if layer else None, _ptr(out.rstd), pack,
+          _ptr(pk.q) if pk is not None else None, _ptr(pk.scale) if pk is not None else None)
+    return out
+
+
+@dataclass
+class NormGrad:
+    d_x: torch.Tensor             # bf16 [rows, d_model]
+    d_weight: Optional[torch.Tensor]
+    d_bias: Optional[torch.Tensor]
+    workspace: torch.Tensor       # uint8
+
+
+def norm_bwd_workspace_size(rows: int, d_model: int) -> int:
+    return int(lib().dlm_norm_bwd_workspace_size(rows, d_model))
+
+
+def norm_bwd(d_y: torch.Tensor, x, rstd: torch.Tensor, mean: Optional[torch.Tensor] = None,
+             weight: Optional[torch.Tensor] = None, kind: int = NORM_LAYER, weight_offset: float = 0.0,
+             want_d_weight: Optional[bool] = None, want_d_bias: bool = False,
+             grad_dtype: Optional[torch.dtype] = None, d_weight: Optional[torch.Tensor] = None,
+             d_bias: Optional[torch.Tensor] = None, accumulate: bool = False, d_x: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None) -> NormGrad:
+    """Backward pass of norm_fwd (see dlm_norm_bwd).  x: norm_fwd's input, or
+    a Packed8 of it (norm_fwd's `packed`).  d_weight (by default when there is
+    a weight) and d_bias (with want_d_bias) come in grad_dtype (by default the
+    weight's type, else float32) or in the tensors given, which accumulate
+    adds to."""
+    _check(d_y, torch.bfloat16, "d_y", min_rows=0)
+    rows, D = d_y.shape
+    ld_dy = _check_rows(d_y, torch.bfloat16, "d_y", rows, D)
+    pt = _check_params(weight, None, D)
+    packed = isinstance(x, Packed8)
+    if packed:
+        _check_packed(x, rows, D, "x")
+        xs, ld_x, fmt, q, qs = None, 0, x.format, x.q, x.scale
+    else:
+        ld_x = _check_rows(x, torch.bfloat16, "x", rows, D)
+        xs, fmt, q, qs = x, PACK_NONE, None, None
+    layer = kind == NORM_LAYER
+    if layer:
+        _check(mean, torch.float32, "mean", min_numel=rows)
+    _check(rstd, torch.float32, "rstd", min_numel=rows)
+    if want_d_weight is None:
+        want_d_weight = weight is not None
+    want_w, want_b = want_d_weight or d_weight is not None, want_d_bias or d_bias is not None
+    if accumulate and (want_w and d_weight is None or want_b and d_bias is None):
+        raise ValueError("accumulate needs d_weight and d_bias for the gradients asked for")
+    for t, name in ((d_weight, "d_weight"), (d_bias, "d_bias")):
+        if t is not None:
+            _param_dtype(t.dtype, name)
+            _check(t, t.dtype, name, min_numel=0)
+            if tuple(t.shape) != (D,):
+                raise ValueError(f"{name}: must have shape ({D},), has {tuple(t.shape)}")
+            if grad_dtype is not None and t.dtype != grad_dtype:
+                raise TypeError(f"{name}: expected {grad_dtype}, got {t.dtype}")
+            grad_dtype = t.dtype
+    if grad_dtype is None:
+        grad_dtype = weight.dtype if weight is not None else torch.float32
+    gt = _param_dtype(grad_dtype, "grad_dtype")
+    ld_dx = D if d_x is None else _check_rows(d_x, torch.bfloat16, "d_x", rows, D)
+    if workspace is not None:
+        _check(workspace, torch.uint8, "workspace", min_numel=0)
+    _on_cuda(d_y=d_y, x=xs, q=q, scale=qs, mean=mean if layer else None, rstd=rstd, weight=weight, d_x=d_x,
+             d_weight=d_weight, d_bias=d_bias, workspace=workspace)
+    dev = d_y.device
+    if d_x is None:
+        d_x = torch.empty((rows, D), dtype=torch.bfloat16, device=dev)
+    if want_w and d_weight is None:
+        d_weight = torch.empty(D, dtype=grad_dtype, device=dev)
+    if want_b and d_bias is None:
+        d_bias = torch.empty(D, dtype=grad_dtype, device=dev)
+    if workspace is None:
+        workspace = _aligned_workspace(norm_bwd_workspace_size(rows, D), dev, 256)
+    _call(dev, "dlm_norm_bwd", _ptr(d_y), ld_dy, _ptr(xs), ld_x, fmt, _ptr(q), _ptr(qs),
+          _ptr(mean) if layer else None, _ptr(rstd), _ptr(weight), pt, kind, weight_offset, rows, D, _ptr(d_x), ld_dx,
+          gt, int(accumulate), _ptr(d_weight), _ptr(d_bias), _ptr(workspace), workspace.numel())
+    return NormGrad(d_x, d_weight, d_bias, workspace)
+
+
+# --------------------------------------------------------------------------
 # autograd wrappers
 # --------------------------------------------------------------------------
 def scale_bf16_(x: torch.Tensor, scale: torch.Tensor) -> torch.Tensor:
@@ -718,3 +1049,55 @@ def decision_loss(logits: torch.Tensor, vocab: int, cand_off: torch.Tensor, cand
         raise ValueError("logits: [n_slots, vocab], one row per label slot")
     return _DecisionLossFn.apply(logits, vocab, cand_off, cand_ids, label_kind, label_val, label_softmax,
                                  brier_weight, hard_label_smoothing)
+
+
+class _EmbedFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, weight, layout, ids, scale):
+        ctx.save_for_backward(ids)
+        ctx.args = (layout, weight.shape[0], scale)
+        return embed_fwd(layout, ids, weight, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        (ids,) = ctx.saved_tensors
+        layout, vocab, scale = ctx.args
+        return (embed_bwd(layout, ids, _as_rows(grad), vocab, scale).d_weight,) + (None,) * 3
+
+
+def embed(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """embed_fwd as a differentiable function of `weight`; its gradient is
+    dense, bf16 [vocab, d_model] (embed_bwd can add it to another one)."""
+    return _EmbedFn.apply(weight, layout, ids, scale)
+
+
+class _NormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, kind, weight_offset, keep8):
+        out = norm_fwd(x, weight, bias, eps, kind, weight_offset,
+                       pack=keep8 if any(ctx.needs_input_grad[:3]) else PACK_NONE)
+        p = out.packed
+        ctx.args = (kind, weight_offset, keep8, None if bias is None else bias.dtype)
+        ctx.save_for_backward(weight, out.mean, out.rstd, *((x, None) if p is None else (p.q, p.scale)))
+        return out.y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        weight, mean, rstd, a, scale = ctx.saved_tensors
+        kind, weight_offset, keep8, bias_dtype = ctx.args
+        g = norm_bwd(_as_rows(grad), a if scale is None else Packed8(a, scale, keep8), rstd, mean, weight, kind,
+                     weight_offset, want_d_weight=ctx.needs_input_grad[1], want_d_bias=ctx.needs_input_grad[2],
+                     grad_dtype=bias_dtype if weight is None else weight.dtype)
+        return (g.d_x, g.d_weight, g.d_bias) + (None,) * 4
+
+
+def norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+         eps: float = 1e-5, kind: int = NORM_LAYER, weight_offset: float = 0.0,
+         keep8: int = PACK_NONE) -> torch.Tensor:
+    """norm_fwd as a differentiable function of `x`, `weight` and `bias`.
+    keep8 = PACK_INT8 or PACK_E4M3: x is kept for the backward pass in 8 bits,
+    written by the forward kernel, in place of x itself; the backward pass then
+    takes those values for x (mean and rstd stay those of x)."""
+    return _NormFn.apply(x, weight, bias, eps, kind, weight_offset, keep8)

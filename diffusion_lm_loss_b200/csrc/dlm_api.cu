@@ -78,7 +78,7 @@ extern "C" const char* dlm_status_string(dlm_status_t status) {
     }
 }
 
-extern "C" int dlm_version(void) { return 200; }   // 0.2.0: + dlm_loss_fwd_bwd_ex
+extern "C" int dlm_version(void) { return 300; }   // 0.3.0: + embedding, norm, 8-bit activations
 
 extern "C" const char* dlm_last_cuda_error(void) { return dlm::g_last_error; }
 

@@ -1,0 +1,625 @@
+// dlm_norm.cu -- layer norm and RMS norm, forward and backward.
+//
+//   mean = (1/d) sum x              (RMS: 0)
+//   rstd = (mean((x - mean)^2) + eps)^(-1/2)
+//   xh = (x - mean) rstd,  y = xh (w + offset) + b
+//   g = dy (w + offset)
+//   dx = rstd (g - mean(g) - xh mean(g xh))     (RMS: without mean(g))
+//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// Forward: a row stays in the registers of the warps that hold it, so mean
+// and the centred sum of squares take two exchanges and one read of x; the
+// 8-bit checkpoint of x is written from the same registers.
+// Backward: each group of warps walks over rows with its columns' dw and db in
+// fp32 registers and leaves one partial row at the end; k_norm_join adds the
+// partial rows in a fixed order.  x comes as bf16 or from its 8-bit
+// checkpoint.
+// Rows too wide or not on 16-byte borders take kernels that read by element
+// or walk over the row more than once.
+#include "dlm_host.h"
+#include "dlm_pack8.cuh"
+
+namespace dlm {
+
+struct NormFwdArgs {
+    const uint16_t* x;
+    int64_t rows, ld_x;
+    int d;
+    const void* w;
+    const void* b;
+    int param_f32, rms;
+    float eps, offset;
+    uint16_t* y;
+    int64_t ld_y;
+    float* mean;
+    float* rstd;
+    int format;            // 0: no checkpoint
+    uint8_t* q;
+    float* q_scale;
+};
+
+struct NormBwdArgs {
+    const uint16_t* dy;
+    int64_t ld_dy;
+    const uint16_t* x;     // NULL: from q, q_scale
+    int64_t ld_x;
+    int format;
+    const uint8_t* q;
+    const float* q_scale;
+    const float* mean;
+    const float* rstd;
+    const void* w;
+    int param_f32, rms;
+    float offset;
+    int64_t rows;
+    int d;
+    uint16_t* dx;
+    int64_t ld_dx;
+    float* part;           // [partial rows][2][pitch]: dw, db
+    int pitch;
+    int want_dw, want_db;
+};
+
+__device__ __forceinline__ float param_at(const void* p, int f32, int c) {
+    return f32 ? __ldg(static_cast<const float*>(p) + c) : bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(p) + c));
+}
+
+// kVec consecutive parameters from column c on; `none` where there is no array
+template <int kVec>
+__device__ __forceinline__ void load_params(const void* p, int f32, int c, float none, float (&o)[kVec]) {
+    if (!p) {
+        #pragma unroll
+        for (int k = 0; k < kVec; ++k) o[k] = none;
+    } else if constexpr (kVec == 8) {
+        if (f32) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
+            o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w; o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+        } else {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c));
+            const uint32_t t[4] = {v.x, v.y, v.z, v.w};
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) { o[2 * k] = bf16lo(t[k]); o[2 * k + 1] = bf16hi(t[k]); }
+        }
+    } else {
+        o[0] = param_at(p, f32, c);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+// Sum over the kNW warps of a row's group; `slot`: a place in shared memory of
+// kNW floats per group that no earlier exchange still reads.
+template <int kNW>
+__device__ __forceinline__ float group_sum(float v, float* slot, int warp_in_group) {
+    v = warp_sum(v);
+    if constexpr (kNW > 1) {
+        if ((threadIdx.x & 31) == 0) slot[warp_in_group] = v;
+        __syncthreads();
+        v = 0.f;
+        #pragma unroll
+        for (int w = 0; w < kNW; ++w) v += slot[w];
+    }
+    return v;
+}
+
+// Groups of kNW warps per CTA: at least 4 warps a CTA.
+constexpr int groups_per_cta(int nw) { return nw >= 4 ? 1 : 4 / nw; }
+
+// ---------------------------------------------------------------------------
+// forward: a row in the registers of kNW warps, kN pieces of kVec elements a lane
+// ---------------------------------------------------------------------------
+template <int kVec, int kN, int kNW>
+__global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd(NormFwdArgs a) {
+    constexpr int kG = groups_per_cta(kNW);
+    __shared__ float s_x[2][kG][kNW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = warp / kNW, wg = warp % kNW;
+    const int t = wg * 32 + lane;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t want = int64_t(blockIdx.x) * kG + g;
+    const bool live = want < a.rows;
+    const int64_t row = live ? want : a.rows - 1;       // a group without a row follows the barriers
+    const uint16_t* x = a.x + row * a.ld_x;
+    uint4 raw[kN];
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const int c = (j * kNW * 32 + t) * kVec;
+        raw[j] = make_uint4(0, 0, 0, 0);
+        if (c < a.d) {
+            if constexpr (kVec == 8) raw[j] = __ldg(reinterpret_cast<const uint4*>(x + c));
+            else raw[j].x = __ldg(x + c);
+        }
+    }
+    float f[kN][kVec];
+    float sum = 0.f;
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        if constexpr (kVec == 8) {
+            const uint32_t w4[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) { f[j][2 * k] = bf16lo(w4[k]); f[j][2 * k + 1] = bf16hi(w4[k]); }
+        } else {
+            f[j][0] = bf16_bits_to_float(uint16_t(raw[j].x));
+        }
+        #pragma unroll
+        for (int k = 0; k < kVec; ++k) sum += f[j][k];
+    }
+    const float inv_d = 1.0f / float(a.d);
+    float mean = 0.f;
+    if (!a.rms) mean = group_sum<kNW>(sum, s_x[0][g], wg) * inv_d;
+    float sq = 0.f;
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const bool in = (j * kNW * 32 + t) * kVec < a.d;
+        #pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            const float v = in ? f[j][k] - mean : 0.f;
+            sq += v * v;
+        }
+    }
+    const float rstd = rsqrtf(group_sum<kNW>(sq, s_x[1][g], wg) * inv_d + a.eps);
+    if (live && t == 0) {
+        if (!a.rms) a.mean[row] = mean;
+        a.rstd[row] = rstd;
+    }
+    uint16_t* y = a.y + row * a.ld_y;
+    const float offset = a.w ? a.offset : 0.f;
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const int c = (j * kNW * 32 + t) * kVec;
+        const bool in = live && c < a.d;
+        if constexpr (kVec == 8) {
+            if (a.format) {                             // 16 lanes hold a block of 128 columns
+                const PackFactors pf = pack_factors(absmax_half_warp(absmax8(raw[j])), a.format);
+                if (in) {
+                    *reinterpret_cast<uint2*>(a.q + row * a.d + c) = pack8_codes(raw[j], pf, a.format);
+                    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+                    if ((lane & 15) == 0) a.q_scale[row * nb + c / DLM_PACK_BLOCK] = pf.scale;
+                }
+            }
+        }
+        if (!in) continue;
+        float w[kVec], b[kVec], o[kVec];
+        load_params<kVec>(a.w, a.param_f32, c, 1.f, w);
+        load_params<kVec>(a.b, a.param_f32, c, 0.f, b);
+        #pragma unroll
+        for (int k = 0; k < kVec; ++k) o[k] = (f[j][k] - mean) * rstd * (w[k] + offset) + b[k];
+        if constexpr (kVec == 8)
+            *reinterpret_cast<uint4*>(y + c) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                                          pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+        else
+            y[c] = __bfloat16_as_ushort(__float2bfloat16_rn(o[0]));
+    }
+}
+
+// Any width and alignment: a CTA per row, which it reads up to three times
+// (from L2 after the first).
+constexpr int kWideThreads = 512;
+
+__device__ __forceinline__ float cta_sum(float v, float* s) {
+    v = warp_sum(v);
+    __syncthreads();                  // earlier readers of s are done
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int w = 0; w < kWideThreads / 32; ++w) v += s[w];
+    return v;
+}
+
+__global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(NormFwdArgs a) {
+    __shared__ float s[kWideThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const float inv_d = 1.0f / float(a.d);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const uint16_t* x = a.x + row * a.ld_x;
+        float mean = 0.f, v = 0.f;
+        if (!a.rms) {
+            for (int c = threadIdx.x; c < a.d; c += kWideThreads) v += bf16_bits_to_float(__ldg(x + c));
+            mean = cta_sum(v, s) * inv_d;
+        }
+        v = 0.f;
+        for (int c = threadIdx.x; c < a.d; c += kWideThreads) {
+            const float u = bf16_bits_to_float(__ldg(x + c)) - mean;
+            v += u * u;
+        }
+        const float rstd = rsqrtf(cta_sum(v, s) * inv_d + a.eps);
+        if (threadIdx.x == 0) {
+            if (!a.rms) a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        for (int c = threadIdx.x; c < a.d; c += kWideThreads) {
+            const float w = a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f;
+            const float b = a.b ? param_at(a.b, a.param_f32, c) : 0.f;
+            a.y[row * a.ld_y + c] = __bfloat16_as_ushort(
+                __float2bfloat16_rn((bf16_bits_to_float(__ldg(x + c)) - mean) * rstd * w + b));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+constexpr int kBwdN = 8;              // elements a lane: one 16-byte piece, or eight 32 * kNW apart
+
+template <int kVec, int kNW>
+__device__ __forceinline__ int bwd_col(int t, int k) {
+    return kVec == 8 ? t * 8 + k : k * kNW * 32 + t;
+}
+
+// x (or its checkpoint's value) and dy of this thread's columns, fp32
+template <int kVec, int kNW>
+__device__ __forceinline__ void bwd_load(const NormBwdArgs& a, int64_t row, int t, float (&x)[kBwdN], float (&dy)[kBwdN]) {
+    if constexpr (kVec == 8) {
+        const int c = t * 8;
+        #pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = dy[k] = 0.f;
+        if (c >= a.d) return;
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.dy + row * a.ld_dy + c));
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        if (a.x) {
+            const uint4 z = __ldg(reinterpret_cast<const uint4*>(a.x + row * a.ld_x + c));
+            const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) { x[2 * k] = bf16lo(w[k]); x[2 * k + 1] = bf16hi(w[k]); }
+        } else {
+            const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+            const uint2 z = __ldg(reinterpret_cast<const uint2*>(a.q + row * a.d + c));
+            const float s = __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK);
+            float lo[4], hi[4];
+            unpack_codes(z.x, a.format, lo);
+            unpack_codes(z.y, a.format, hi);
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) { x[k] = lo[k] * s; x[4 + k] = hi[k] * s; }
+        }
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) { dy[2 * k] = bf16lo(u[k]); dy[2 * k + 1] = bf16hi(u[k]); }
+    } else {
+        #pragma unroll
+        for (int k = 0; k < kBwdN; ++k) {
+            const int c = bwd_col<kVec, kNW>(t, k);
+            x[k] = dy[k] = 0.f;
+            if (c < a.d) {
+                dy[k] = bf16_bits_to_float(__ldg(a.dy + row * a.ld_dy + c));
+                if (a.x) {
+                    x[k] = bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c));
+                } else {
+                    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+                    x[k] = unpack_code(__ldg(a.q + row * a.d + c), a.format) *
+                           __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK);
+                }
+            }
+        }
+    }
+}
+
+template <int kVec, int kNW>
+__global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_bwd(NormBwdArgs a) {
+    constexpr int kG = groups_per_cta(kNW);
+    constexpr int kR = 2;              // rows at a time: their loads overlap, their sums share a barrier
+    __shared__ float s_x[2][kG][kNW][2 * kR];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = warp / kNW, wg = warp % kNW;
+    const int t = wg * 32 + lane;
+    float w[kBwdN], dw[kBwdN], db[kBwdN];
+    pdl_wait();
+    pdl_launch_dependents();
+    #pragma unroll
+    for (int k = 0; k < kBwdN; ++k) {
+        const int c = bwd_col<kVec, kNW>(t, k);
+        w[k] = c < a.d ? (a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f) : 0.f;
+        dw[k] = db[k] = 0.f;
+    }
+    const float inv_d = 1.0f / float(a.d);
+    const int64_t groups = int64_t(gridDim.x) * kG;
+    // every group of a CTA makes the same number of turns (barriers)
+    const int64_t turns = (a.rows + groups * kR - 1) / (groups * kR);
+    int buf = 0;
+    for (int64_t i = 0; i < turns; ++i, buf ^= 1) {
+        const int64_t r0 = (i * groups + int64_t(blockIdx.x) * kG + g) * kR;
+        float x[kR][kBwdN], dy[kR][kBwdN], rstd[kR], s1[kR], s2[kR];
+        #pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const bool live = r0 + r < a.rows;
+            const int64_t row = live ? r0 + r : a.rows - 1;
+            bwd_load<kVec, kNW>(a, row, t, x[r], dy[r]);
+            const float mean = a.rms ? 0.f : __ldg(a.mean + row);
+            rstd[r] = __ldg(a.rstd + row);
+            s1[r] = s2[r] = 0.f;
+            #pragma unroll
+            for (int k = 0; k < kBwdN; ++k) {
+                const float xh = (x[r][k] - mean) * rstd[r];
+                x[r][k] = xh;
+                const float gk = dy[r][k] * w[k];
+                s1[r] += gk;
+                s2[r] += bwd_col<kVec, kNW>(t, k) < a.d ? gk * xh : 0.f;
+                if (live && bwd_col<kVec, kNW>(t, k) < a.d) {
+                    dw[k] += dy[r][k] * xh;
+                    db[k] += dy[r][k];
+                }
+            }
+            s1[r] = warp_sum(s1[r]);
+            s2[r] = warp_sum(s2[r]);
+        }
+        if constexpr (kNW > 1) {
+            if (lane == 0) {
+                #pragma unroll
+                for (int r = 0; r < kR; ++r) { s_x[buf][g][wg][2 * r] = s1[r]; s_x[buf][g][wg][2 * r + 1] = s2[r]; }
+            }
+            __syncthreads();
+            #pragma unroll
+            for (int r = 0; r < kR; ++r) s1[r] = s2[r] = 0.f;
+            #pragma unroll
+            for (int v = 0; v < kNW; ++v) {
+                #pragma unroll
+                for (int r = 0; r < kR; ++r) { s1[r] += s_x[buf][g][v][2 * r]; s2[r] += s_x[buf][g][v][2 * r + 1]; }
+            }
+        }
+        #pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            if (r0 + r >= a.rows) break;
+            const float m1 = a.rms ? 0.f : s1[r] * inv_d, m2 = s2[r] * inv_d;
+            uint16_t* dx = a.dx + (r0 + r) * a.ld_dx;
+            float o[kBwdN];
+            #pragma unroll
+            for (int k = 0; k < kBwdN; ++k) o[k] = (dy[r][k] * w[k] - m1 - x[r][k] * m2) * rstd[r];
+            if constexpr (kVec == 8) {
+                if (t * 8 < a.d)
+                    *reinterpret_cast<uint4*>(dx + t * 8) =
+                        make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                   pack_bf16x2(o[6], o[7]));
+            } else {
+                #pragma unroll
+                for (int k = 0; k < kBwdN; ++k)
+                    if (bwd_col<kVec, kNW>(t, k) < a.d)
+                        dx[bwd_col<kVec, kNW>(t, k)] = __bfloat16_as_ushort(__float2bfloat16_rn(o[k]));
+            }
+        }
+    }
+    float* part = a.part + (int64_t(blockIdx.x) * kG + g) * 2 * a.pitch;
+    #pragma unroll
+    for (int k = 0; k < kBwdN; ++k) {
+        const int c = bwd_col<kVec, kNW>(t, k);
+        if (c < a.d) {
+            if (a.want_dw) part[c] = dw[k];
+            if (a.want_db) part[a.pitch + c] = db[k];
+        }
+    }
+}
+
+// Any width and alignment: a CTA walks over its rows twice each and keeps its
+// partial row in the workspace, which only it touches.
+__global__ void __launch_bounds__(kWideThreads) k_norm_bwd_wide(NormBwdArgs a) {
+    __shared__ float s[kWideThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const float inv_d = 1.0f / float(a.d);
+    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+    float* part = a.part + int64_t(blockIdx.x) * 2 * a.pitch;
+    bool first = true;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false) {
+        const float mean = a.rms ? 0.f : a.mean[row], rstd = a.rstd[row];
+        auto xh_at = [&](int c) {
+            const float x = a.x ? bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c))
+                                : unpack_code(__ldg(a.q + row * a.d + c), a.format) *
+                                      __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK);
+            return (x - mean) * rstd;
+        };
+        float s1 = 0.f, s2 = 0.f;
+        for (int c = threadIdx.x; c < a.d; c += kWideThreads) {
+            const float xh = xh_at(c), dy = bf16_bits_to_float(__ldg(a.dy + row * a.ld_dy + c));
+            const float g = dy * (a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f);
+            s1 += g;
+            s2 += g * xh;
+            if (a.want_dw) part[c] = (first ? 0.f : part[c]) + dy * xh;
+            if (a.want_db) part[a.pitch + c] = (first ? 0.f : part[a.pitch + c]) + dy;
+        }
+        s1 = cta_sum(s1, s);
+        s2 = cta_sum(s2, s);
+        const float m1 = a.rms ? 0.f : s1 * inv_d, m2 = s2 * inv_d;
+        for (int c = threadIdx.x; c < a.d; c += kWideThreads) {
+            const float dy = bf16_bits_to_float(__ldg(a.dy + row * a.ld_dy + c));
+            const float g = dy * (a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f);
+            a.dx[row * a.ld_dx + c] = __bfloat16_as_ushort(__float2bfloat16_rn((g - m1 - xh_at(c) * m2) * rstd));
+        }
+    }
+}
+
+// dw (blockIdx.y = 0) and db (1) from the partial rows: a lane per column, the
+// warps take consecutive parts of the rows.
+constexpr int kNormJoinWarps = 8;
+
+__global__ void __launch_bounds__(kNormJoinWarps * 32) k_norm_join(const float* __restrict__ part, int n_part,
+                                                                   int pitch, int d, int grad_f32, int accumulate,
+                                                                   void* __restrict__ d_weight,
+                                                                   void* __restrict__ d_bias) {
+    __shared__ float s[kNormJoinWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    void* out = blockIdx.y ? d_bias : d_weight;
+    pdl_wait();
+    if (!out) return;
+    const int per = (n_part + kNormJoinWarps - 1) / kNormJoinWarps;
+    const int k0 = min(n_part, warp * per), k1 = min(n_part, k0 + per);
+    float acc = 0.f;
+    if (c < d) {
+        const float* p = part + blockIdx.y * pitch + c;
+        #pragma unroll 8
+        for (int k = k0; k < k1; ++k) acc += p[int64_t(k) * 2 * pitch];
+    }
+    s[warp][lane] = acc;
+    __syncthreads();
+    if (warp || c >= d) return;
+    acc = 0.f;
+    #pragma unroll
+    for (int w = 0; w < kNormJoinWarps; ++w) acc += s[w][lane];
+    if (grad_f32) {
+        float* o = static_cast<float*>(out) + c;
+        *o = accumulate ? *o + acc : acc;
+    } else {
+        uint16_t* o = static_cast<uint16_t*>(out) + c;
+        *o = __bfloat16_as_ushort(__float2bfloat16_rn(accumulate ? bf16_bits_to_float(*o) + acc : acc));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+static bool finite_f(float v) { return v - v == 0.0f; }
+
+static bool param_aligned(const void* p) { return !p || aligned16(p); }
+
+template <int kVec, int kN, int kNW>
+static dlm_status_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
+    constexpr int kG = groups_per_cta(kNW);
+    return launch_pdl(k_norm_fwd<kVec, kN, kNW>, dim3(unsigned((a.rows + kG - 1) / kG)), dim3(kNW * kG * 32), 0, s,
+                      "k_norm_fwd launch", a);
+}
+
+// warps that a row of `pieces` pieces takes at `per` pieces a lane: a power of
+// two up to 32, 0 if they do not hold it
+static int warps_for(int64_t pieces, int per) {
+    for (int nw = 1; nw <= 32; nw *= 2)
+        if (pieces <= int64_t(nw) * 32 * per) return nw;
+    return 0;
+}
+
+template <int kVec, int kN>
+static dlm_status_t launch_fwd_n(int nw, const NormFwdArgs& a, cudaStream_t s) {
+    switch (nw) {
+        case 1: return launch_fwd<kVec, kN, 1>(a, s);
+        case 2: return launch_fwd<kVec, kN, 2>(a, s);
+        case 4: return launch_fwd<kVec, kN, 4>(a, s);
+        case 8: return launch_fwd<kVec, kN, 8>(a, s);
+        case 16: return launch_fwd<kVec, kN, 16>(a, s);
+        default: return launch_fwd<kVec, kN, 32>(a, s);
+    }
+}
+
+template <int kVec, int kNW>
+static dlm_status_t launch_bwd(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
+    return launch_pdl(k_norm_bwd<kVec, kNW>, dim3(grid), dim3(kNW * groups_per_cta(kNW) * 32), 0, s,
+                      "k_norm_bwd launch", a);
+}
+
+template <int kVec>
+static dlm_status_t launch_bwd_n(int nw, const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
+    switch (nw) {
+        case 1: return launch_bwd<kVec, 1>(a, grid, s);
+        case 2: return launch_bwd<kVec, 2>(a, grid, s);
+        case 4: return launch_bwd<kVec, 4>(a, grid, s);
+        case 8: return launch_bwd<kVec, 8>(a, grid, s);
+        case 16: return launch_bwd<kVec, 16>(a, grid, s);
+        default: return launch_bwd<kVec, 32>(a, grid, s);
+    }
+}
+
+// How the backward pass splits its rows (by the width alone, so that the
+// workspace does not depend on alignment: the scalar and the vector kernel
+// hold eight elements a lane alike).
+struct NormBwdPlan { int nw; unsigned grid; int partials; int pitch; size_t bytes; };
+
+static bool norm_bwd_plan(int64_t rows, int32_t d, NormBwdPlan* p) {
+    if (rows < 0 || d < 1 || d > INT32_MAX - 128) return false;
+    p->nw = warps_for(d, kBwdN);
+    const int groups = p->nw ? groups_per_cta(p->nw) : 1;
+    const int threads = p->nw ? p->nw * groups * 32 : kWideThreads;
+    const int64_t resident = 148 * int64_t(1024 / threads);
+    const int64_t need = (rows + groups - 1) / groups;
+    p->grid = unsigned(need < resident ? need : resident);
+    p->partials = int(p->grid) * groups;
+    p->pitch = int(align_up(size_t(d), 32));
+    p->bytes = align_up((size_t(p->partials) * 2 + 1) * size_t(p->pitch) * 4, kWsAlign);
+    return true;
+}
+
+}  // namespace dlm
+
+using namespace dlm;
+
+extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_model, int64_t ld_x,
+                                     const void* weight, const void* bias, int32_t param_dtype, int32_t kind,
+                                     float eps, float weight_offset, uint16_t* y, int64_t ld_y, float* mean,
+                                     float* rstd, int32_t pack_format, uint8_t* q, float* q_scale,
+                                     dlm_stream_t stream) {
+    DLM_NVTX("dlm_norm_fwd");
+    if (rows < 0 || d_model < 1 || d_model > INT32_MAX - 128 || ld_x < d_model || ld_y < d_model)
+        return DLM_ERR_INVALID_ARGUMENT;
+    if (kind != DLM_NORM_LAYER && kind != DLM_NORM_RMS) return DLM_ERR_INVALID_ARGUMENT;
+    if (param_dtype != DLM_BF16 && param_dtype != DLM_F32) return DLM_ERR_INVALID_ARGUMENT;
+    if (!(eps >= 0.0f) || !finite_f(eps) || !finite_f(weight_offset)) return DLM_ERR_INVALID_ARGUMENT;
+    if (pack_format != DLM_PACK_NONE && pack_format != DLM_PACK_INT8 && pack_format != DLM_PACK_E4M3)
+        return DLM_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return DLM_OK;
+    if (!x || !y || !rstd || (kind == DLM_NORM_LAYER && !mean)) return DLM_ERR_INVALID_ARGUMENT;
+    if (pack_format != DLM_PACK_NONE && (!q || !q_scale)) return DLM_ERR_INVALID_ARGUMENT;
+    if (rows > INT32_MAX) return DLM_ERR_INVALID_ARGUMENT;
+    dlm_status_t st = check_device();
+    if (st != DLM_OK) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    NormFwdArgs a = {x, rows, ld_x, d_model, weight, bias, param_dtype == DLM_F32, kind == DLM_NORM_RMS, eps,
+                     weight_offset, y, ld_y, mean, rstd, pack_format, q, q_scale};
+    const bool vec = d_model % 8 == 0 && ld_x % 8 == 0 && ld_y % 8 == 0 && aligned16(x) && aligned16(y) &&
+                     param_aligned(weight) && param_aligned(bias) && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
+    const int nw = vec ? warps_for(d_model / 8, 4) : warps_for(d_model, 8);
+    if (vec && nw) return launch_fwd_n<8, 4>(nw, a, s);
+    if (nw) st = launch_fwd_n<1, 8>(nw, a, s);
+    else st = launch_pdl(k_norm_fwd_wide, dim3(unsigned(rows < 148 * 4 ? rows : 148 * 4)), dim3(kWideThreads), 0, s,
+                         "k_norm_fwd_wide launch", a);
+    if (st != DLM_OK || pack_format == DLM_PACK_NONE) return st;
+    return dlm_pack8(x, rows, d_model, ld_x, pack_format, q, q_scale, stream);
+}
+
+extern "C" size_t dlm_norm_bwd_workspace_size(int64_t rows, int32_t d_model) {
+    NormBwdPlan p;
+    return norm_bwd_plan(rows, d_model, &p) ? p.bytes : 0;
+}
+
+extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const uint16_t* x, int64_t ld_x,
+                                     int32_t pack_format, const uint8_t* q, const float* q_scale, const float* mean,
+                                     const float* rstd, const void* weight, int32_t param_dtype, int32_t kind,
+                                     float weight_offset, int64_t rows, int32_t d_model, uint16_t* d_x,
+                                     int64_t ld_dx, int32_t grad_dtype, int32_t accumulate, void* d_weight,
+                                     void* d_bias, void* workspace, size_t workspace_bytes, dlm_stream_t stream) {
+    DLM_NVTX("dlm_norm_bwd");
+    NormBwdPlan p;
+    if (!norm_bwd_plan(rows, d_model, &p)) return DLM_ERR_INVALID_ARGUMENT;
+    if (ld_dy < d_model || ld_dx < d_model) return DLM_ERR_INVALID_ARGUMENT;
+    if (kind != DLM_NORM_LAYER && kind != DLM_NORM_RMS) return DLM_ERR_INVALID_ARGUMENT;
+    if ((param_dtype != DLM_BF16 && param_dtype != DLM_F32) || (grad_dtype != DLM_BF16 && grad_dtype != DLM_F32))
+        return DLM_ERR_INVALID_ARGUMENT;
+    if ((accumulate != 0 && accumulate != 1) || !finite_f(weight_offset)) return DLM_ERR_INVALID_ARGUMENT;
+    if (pack_format == DLM_PACK_NONE) {
+        if (ld_x < d_model || (rows > 0 && !x)) return DLM_ERR_INVALID_ARGUMENT;
+    } else if ((pack_format != DLM_PACK_INT8 && pack_format != DLM_PACK_E4M3) || (rows > 0 && (!q || !q_scale))) {
+        return DLM_ERR_INVALID_ARGUMENT;
+    }
+    if (rows > 0 && (!d_y || !d_x || !rstd || (kind == DLM_NORM_LAYER && !mean))) return DLM_ERR_INVALID_ARGUMENT;
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kWsAlign) return DLM_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < p.bytes) return DLM_ERR_WORKSPACE_TOO_SMALL;
+    dlm_status_t st = check_device();
+    if (st != DLM_OK) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    NormBwdArgs a = {d_y, ld_dy, pack_format == DLM_PACK_NONE ? x : nullptr, ld_x, pack_format, q, q_scale, mean,
+                     rstd, weight, param_dtype == DLM_F32, kind == DLM_NORM_RMS, weight_offset, rows, d_model, d_x,
+                     ld_dx, static_cast<float*>(workspace), p.pitch,
+                     d_weight != nullptr, d_bias != nullptr};
+    if (rows > 0) {
+        const bool vec = d_model % 8 == 0 && ld_dy % 8 == 0 && ld_dx % 8 == 0 && aligned16(d_y) && aligned16(d_x) &&
+                         (a.x ? ld_x % 8 == 0 && aligned16(x) : (reinterpret_cast<uintptr_t>(q) & 7) == 0);
+        if (!p.nw) st = launch_pdl(k_norm_bwd_wide, dim3(p.grid), dim3(kWideThreads), 0, s, "k_norm_bwd_wide launch", a);
+        else if (vec) st = launch_bwd_n<8>(p.nw, a, p.grid, s);
+        else st = launch_bwd_n<1>(p.nw, a, p.grid, s);
+        if (st != DLM_OK) return st;
+    }
+    if (!d_weight && !d_bias) return DLM_OK;
+    return launch_pdl(k_norm_join, dim3(unsigned((d_model + 31) / 32), 2), dim3(kNormJoinWarps * 32), 0, s,
+                      "k_norm_join launch", (const float*)a.part, p.partials, p.pitch, d_model,
+                      int(grad_dtype == DLM_F32), accumulate, d_weight, d_bias);
+}

@@ -21,6 +21,16 @@
  *                            (candidate-restricted CE, full-vocabulary CE,
  *                            Brier), forward + backward
  *
+ * and the operators next to them that a training step of the same model
+ * needs at its two ends:
+ *
+ *   dlm_embed_fwd / _bwd     embedding of the (noisy) ids, with a scale, and
+ *                            the table's gradient
+ *   dlm_norm_fwd / _bwd      layer norm or RMS norm (the one before the output
+ *                            head, and any other), with the weight's and
+ *                            bias's gradients; its input may be kept in 8 bits
+ *   dlm_pack8 / dlm_unpack8  activations held in 8 bits between the passes
+ *
  * The method (page title, section):
  *   "LLaDA-8B-MDLM-LoRA", Training table, row "Objective": t ~ U(0,1) per
  *       sequence, mask probability p = (1 - 1e-3) t + 1e-3, cross-entropy on
@@ -53,6 +63,8 @@
  *     word; the affected rows are treated as unscored and the call still
  *     completes.  Read the word with dlm_get_device_status.
  *   - bf16 tensors are passed as uint16_t bit patterns (IEEE bfloat16).
+ *   - Outputs do not overlap inputs or each other (dlm_scale_bf16 and the
+ *     accumulate options, which update a buffer, apart).
  *   - Requires compute capability 10.0 (B200); other devices get
  *     DLM_ERR_UNSUPPORTED.
  */
@@ -503,6 +515,148 @@ DLM_API dlm_status_t dlm_decision_loss_fwd_bwd(int32_t n_slots, const uint16_t *
  * ---------------------------------------------------------------------- */
 DLM_API dlm_status_t dlm_scale_bf16(uint16_t *x, int64_t rows, int64_t cols, int64_t ld,
                                     const float *scale, dlm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Types of parameters and of their gradients.
+ * ---------------------------------------------------------------------- */
+#define DLM_BF16 0
+#define DLM_F32 1
+
+/* ------------------------------------------------------------------------
+ * dlm_embed_fwd -- embedding of token ids:
+ *   out[i, :] = bf16(scale * weight[ids[i], :]),  i < layout.n_tokens
+ *   weight [vocab, ld_weight] bf16, out [n_tokens, ld_out] bf16 (columns
+ *   0..d_model-1 written), ids int32 (the clean ids, or dlm_corrupt's).
+ * Only layout.n_tokens and layout.pad_mask are read: the ids of pads are not
+ * looked at and their rows are zeros.  An id outside [0, vocab) of a token
+ * that is no pad gives a row of zeros and sets DLM_DEV_BAD_TOKEN_ID in
+ * *dev_status (a device uint32, or'ed; may be NULL).
+ * Errors: a bad layout, vocab or d_model < 1, a row stride < d_model, a scale
+ * that is not finite or a null pointer return DLM_ERR_INVALID_ARGUMENT.
+ * n_tokens = 0 is a no-op.  Rows on 16-byte borders (d_model and strides
+ * multiples of 8, aligned pointers) take 16-byte accesses, others single
+ * elements, with the same results.
+ * The pages have no counterpart: they train whole models, whose input this
+ * is.
+ * ---------------------------------------------------------------------- */
+DLM_API dlm_status_t dlm_embed_fwd(const dlm_layout_t *layout, const int32_t *ids, const uint16_t *weight,
+                                   int64_t ld_weight, int32_t vocab, int32_t d_model, float scale,
+                                   uint16_t *out, int64_t ld_out, uint32_t *dev_status,
+                                   dlm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dlm_embed_bwd -- gradient of the embedding table:
+ *   d_weight[v, :] = scale * sum of d_out[i, :] over the tokens i that are no
+ *                    pads with ids[i] = v
+ * summed in fp32 in an order that depends on the ids alone, and rounded once:
+ * results are bitwise reproducible.
+ *   d_out [n_tokens, ld] bf16; d_weight [vocab, ld_dw] bf16 or float
+ *   (grad_dtype DLM_BF16 / DLM_F32).
+ *   accumulate = 0: every row of d_weight is written (zeros where no token
+ *     has the id).
+ *   accumulate = 1: the sums are added to what d_weight holds, in fp32 with
+ *     one rounding; rows that no token has are neither read nor written (a
+ *     gradient kept over several batches, or a tied output head's d_weight).
+ * Pads' rows of d_out are not read.  Tokens with an id outside [0, vocab) add
+ * nothing and set DLM_DEV_BAD_TOKEN_ID in the status word of the workspace
+ * (dlm_get_device_status).
+ * workspace: at least dlm_embed_bwd_workspace_size() bytes, 256-byte aligned.
+ * Errors: as dlm_embed_fwd; an unknown grad_dtype, accumulate other than 0 or
+ * 1, a misaligned workspace, or sizes whose launch would pass 2^31 blocks
+ * return DLM_ERR_INVALID_ARGUMENT, a workspace that is too small
+ * DLM_ERR_WORKSPACE_TOO_SMALL, before anything is enqueued.
+ * ---------------------------------------------------------------------- */
+DLM_API size_t dlm_embed_bwd_workspace_size(const dlm_layout_t *layout, int32_t d_model, int32_t vocab);
+
+DLM_API dlm_status_t dlm_embed_bwd(const dlm_layout_t *layout, const int32_t *ids, const uint16_t *d_out,
+                                   int64_t ld, int32_t vocab, int32_t d_model, float scale,
+                                   int32_t grad_dtype, int32_t accumulate, void *d_weight, int64_t ld_dw,
+                                   void *workspace, size_t workspace_bytes, dlm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dlm_pack8, dlm_unpack8 -- an activation [rows, cols] bf16 in 8 bits: the
+ * form in which what the backward pass needs is kept between the passes, at
+ * half the memory.
+ * Blocks of DLM_PACK_BLOCK columns of a row (the last one may be shorter)
+ * share one factor.  With a = max |x| over the block, and top = 127
+ * (DLM_PACK_INT8: signed integers) or 448 (DLM_PACK_E4M3: 8-bit floats, 4
+ * exponent and 3 fraction bits), in fp32 with one rounding each:
+ *   scale = a / top,  u = x * (top / a),  code = u rounded to the nearest
+ *   integer or e4m3 value, ties to even;  the value held is code * scale.
+ * A block with a < 2^-100 is held as zeros (scale 0).  A block that has an
+ * infinity or a NaN gets scale NaN: all of it reads back as NaN.
+ *   q [rows, cols] bytes, contiguous; scale [rows, ceil(cols / 128)] float.
+ *   x [rows, ld], out [rows, ld] bf16: unpack writes bf16(code * scale).
+ * Errors: a negative size, ld < cols, an unknown format or a null pointer
+ * return DLM_ERR_INVALID_ARGUMENT; rows or cols = 0 is a no-op.
+ * ---------------------------------------------------------------------- */
+#define DLM_PACK_NONE 0
+#define DLM_PACK_INT8 1
+#define DLM_PACK_E4M3 2
+#define DLM_PACK_BLOCK 128
+
+DLM_API dlm_status_t dlm_pack8(const uint16_t *x, int64_t rows, int32_t cols, int64_t ld, int32_t format,
+                               uint8_t *q, float *scale, dlm_stream_t stream);
+
+DLM_API dlm_status_t dlm_unpack8(const uint8_t *q, const float *scale, int64_t rows, int32_t cols,
+                                 int32_t format, uint16_t *out, int64_t ld, dlm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dlm_norm_fwd -- layer norm (DLM_NORM_LAYER) or RMS norm (DLM_NORM_RMS) of
+ * each row of x [rows, ld_x] bf16, statistics in fp32:
+ *   mean = (1 / d) sum x  (RMS: 0, and `mean` is not written and may be NULL)
+ *   rstd = 1 / sqrt((1 / d) sum (x - mean)^2 + eps)
+ *   y    = (x - mean) * rstd * (weight + weight_offset) + bias, rounded once
+ * weight, bias [d_model] of param_dtype (DLM_BF16 / DLM_F32); weight NULL: a
+ * factor of 1 (weight_offset is not read), bias NULL: none.  weight_offset is
+ * 0, or 1 for weights stored as w - 1.  y [rows, ld_y] bf16; mean, rstd
+ * [rows] float (kept for the backward pass).
+ * pack_format other than DLM_PACK_NONE: q and q_scale get x in the form of
+ * dlm_pack8, in the same pass over x where its rows lie on 16-byte borders
+ * and d_model <= 32,768.
+ * Errors: rows < 0 or >= 2^31, d_model < 1, a row stride < d_model, an
+ * unknown kind, type or format, eps < 0 or not finite, weight_offset not
+ * finite or a null pointer return DLM_ERR_INVALID_ARGUMENT.  rows = 0 is a
+ * no-op.
+ * ---------------------------------------------------------------------- */
+#define DLM_NORM_LAYER 0
+#define DLM_NORM_RMS 1
+
+DLM_API dlm_status_t dlm_norm_fwd(const uint16_t *x, int64_t rows, int32_t d_model, int64_t ld_x,
+                                  const void *weight, const void *bias, int32_t param_dtype, int32_t kind,
+                                  float eps, float weight_offset, uint16_t *y, int64_t ld_y, float *mean,
+                                  float *rstd, int32_t pack_format, uint8_t *q, float *q_scale,
+                                  dlm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dlm_norm_bwd -- backward pass of dlm_norm_fwd.  With xh = (x - mean) rstd
+ * and g = d_y * (weight + weight_offset):
+ *   d_x      = rstd * (g - mean(g) - xh * mean(g * xh))   (RMS: no mean(g))
+ *   d_weight = sum over rows of d_y * xh
+ *   d_bias   = sum over rows of d_y
+ * d_x [rows, ld_dx] bf16, rounded once; d_weight, d_bias [d_model] of
+ * grad_dtype, or NULL to skip them.  accumulate = 1 adds them to what they
+ * hold.  All sums are in fp32 in a fixed order: results are bitwise
+ * reproducible.
+ * x: bf16 with pack_format DLM_PACK_NONE; otherwise x is not read and
+ * q, q_scale (dlm_norm_fwd's, or dlm_pack8's of x) stand for it, each element
+ * code * scale in fp32.  mean and rstd are dlm_norm_fwd's (mean may be NULL
+ * for RMS).
+ * workspace: at least dlm_norm_bwd_workspace_size() bytes, 256-byte aligned.
+ * It has no status word: nothing here depends on device data.
+ * Errors: as dlm_norm_fwd, and a misaligned or (DLM_ERR_WORKSPACE_TOO_SMALL)
+ * too small workspace.  rows = 0 writes zeros to d_weight and d_bias, or
+ * leaves them with accumulate = 1.
+ * ---------------------------------------------------------------------- */
+DLM_API size_t dlm_norm_bwd_workspace_size(int64_t rows, int32_t d_model);
+
+DLM_API dlm_status_t dlm_norm_bwd(const uint16_t *d_y, int64_t ld_dy, const uint16_t *x, int64_t ld_x,
+                                  int32_t pack_format, const uint8_t *q, const float *q_scale,
+                                  const float *mean, const float *rstd, const void *weight,
+                                  int32_t param_dtype, int32_t kind, float weight_offset, int64_t rows,
+                                  int32_t d_model, uint16_t *d_x, int64_t ld_dx, int32_t grad_dtype,
+                                  int32_t accumulate, void *d_weight, void *d_bias, void *workspace,
+                                  size_t workspace_bytes, dlm_stream_t stream);
 
 #ifdef __cplusplus
 }
