@@ -7,15 +7,18 @@
 //   dx = rstd (g - mean(g) - xh mean(g xh))     (RMS: without mean(g))
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 //
-// Forward: a row stays in the registers of the warps that hold it, so mean
-// and the centred sum of squares take two exchanges and one read of x; the
-// 8-bit checkpoint of x is written from the same registers.
-// Backward: each group of warps walks over rows with its columns' dw and db in
-// fp32 registers and leaves one partial row at the end; k_norm_join adds the
-// partial rows in a fixed order.  x comes as bf16 or from its 8-bit
-// checkpoint.
-// Rows too wide or not on 16-byte borders take kernels that read by element
-// or walk over the row more than once.
+// Many rows on 16-byte borders (k_norm_fwd_ring, k_norm_bwd_ring): one CTA of
+// up to 16 warps per SM, split into groups that each hold a whole row; a group
+// walks over its rows while asynchronous copies fill a ring of the next ones
+// in shared memory, each thread copying just the pieces that it will read
+// itself, so that the loads need no barrier of their own and no wait but the
+// copy group's.  A row stays in registers between its sums and its output.
+// Backward: the columns' dw and db stay in fp32 registers over all rows of a
+// group; a CTA leaves one partial row, and k_norm_join adds the partial rows
+// in a fixed order.  x comes as bf16 or from its 8-bit checkpoint.
+// Few rows, rows too wide for a group, rows that are not on 16-byte borders:
+// kernels of one row per group of warps (k_norm_fwd), of single elements
+// (k_norm_bwd), or of any width (k_norm_*_wide).
 #include "dlm_host.h"
 #include "dlm_pack8.cuh"
 
@@ -198,6 +201,354 @@ __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd(Nor
     }
 }
 
+// ---------------------------------------------------------------------------
+// rings of rows
+// ---------------------------------------------------------------------------
+constexpr int kRingThreads = 512;
+
+// How a width is split: `nw` warps hold a row at kN pieces of 8 elements a
+// lane, `groups` of them make a CTA.
+struct RingShape { int nw, groups; };
+
+__device__ __forceinline__ uint64_t f2splat(float v) { return f2pack(v, v); }
+
+// The sums of s1 and s2 over a group, in every lane.  Lanes 0..15 carry s1,
+// 16..31 s2.  slot: [nw] float2 that no earlier exchange still reads; `bar`:
+// the group's barrier.
+__device__ __forceinline__ void group_sum2(float& s1, float& s2, float2* slot, int wg, const RingShape sh, int bar) {
+    const int lane = threadIdx.x & 31;
+    float v = lane < 16 ? s1 : s2;
+    v += __shfl_xor_sync(~0u, lane < 16 ? s2 : s1, 16);
+    #pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    if (sh.nw > 1) {
+        if ((lane & 15) == 0) reinterpret_cast<float*>(slot + wg)[lane >> 4] = v;
+        named_barrier_sync(bar, sh.nw * 32);
+        v = (lane & 15) < sh.nw ? reinterpret_cast<const float*>(slot + (lane & 15))[lane >> 4] : 0.f;
+        #pragma unroll
+        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    }
+    const float other = __shfl_xor_sync(~0u, v, 16);
+    s1 = lane < 16 ? v : other;
+    s2 = lane < 16 ? other : v;
+}
+
+__device__ __forceinline__ float group_sum1(float v, float* slot, int wg, const RingShape sh, int bar) {
+    const int lane = threadIdx.x & 31;
+    v = warp_sum(v);
+    if (sh.nw > 1) {
+        if (lane == 0) slot[wg] = v;
+        named_barrier_sync(bar, sh.nw * 32);
+        v = (lane & 15) < sh.nw ? slot[lane & 15] : 0.f;
+        #pragma unroll
+        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint64_t f2bf16(uint32_t w) { return f2pack(bf16lo(w), bf16hi(w)); }
+
+__device__ __forceinline__ uint32_t f2to_bf16(uint64_t v) {
+    float lo, hi;
+    f2unpack(v, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
+
+// 8 parameters as 4 pairs
+__device__ __forceinline__ void param_pairs(const void* p, int f32, int c, float none, float add, uint64_t (&o)[4]) {
+    #pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = p ? f2pack(param_at(p, f32, c + 2 * k) + add, param_at(p, f32, c + 2 * k + 1) + add) : f2splat(none);
+}
+
+template <int kN>
+constexpr int fwd_stages() { return kN == 1 ? 16 : 10; }
+template <int kN>
+constexpr int bwd_stages() { return kN == 1 ? 10 : 6; }
+
+// A thread's slots of the ring, [stages][pieces] of 16 bytes, the threads side
+// by side.  `in`: the pieces that lie inside the row; the others stay zero.
+template <int kS, int kPieces>
+struct Ring {
+    uint32_t base, pitch, put, get;
+    __device__ __forceinline__ explicit Ring(uint4* smem) {
+        base = smem_addr(smem + threadIdx.x);
+        pitch = blockDim.x * 16u;
+        put = get = base;
+        for (int k = 0; k < kS * kPieces; ++k) smem[threadIdx.x + k * blockDim.x] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void step(uint32_t& at) const {
+        at += kPieces * pitch;
+        if (at == base + uint32_t(kS * kPieces) * pitch) at = base;
+    }
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+
+template <int kN>
+__global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a, RingShape sh) {
+    constexpr int kS = fwd_stages<kN>();
+    extern __shared__ uint4 ring_mem[];
+    __shared__ float s_x[2][2][16];                       // [row parity][sum][warp]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = warp / sh.nw, wg = warp - g * sh.nw;
+    const int t = wg * 32 + lane, gt = sh.nw * 32;
+    uint64_t w[kN][4], b[kN][4];
+    bool in[kN];
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) in[j] = (j * gt + t) * 8 < a.d;
+    Ring<kS, kN> ring(ring_mem);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
+    int n = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
+    const uint16_t* px = a.x + first * a.ld_x + t * 8;
+    int left = n;
+    auto issue = [&]() {
+        if (left > 0) {
+            #pragma unroll
+            for (int j = 0; j < kN; ++j)
+                if (in[j]) cp_async16(ring.put + j * ring.pitch, px + j * gt * 8);
+            px += step * a.ld_x;
+            --left;
+        }
+        cp_async_commit();
+        ring.step(ring.put);
+    };
+    #pragma unroll 1
+    for (int s = 0; s < kS - 1; ++s) issue();
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const int c = in[j] ? (j * gt + t) * 8 : 0;
+        param_pairs(a.w, a.param_f32, c, 1.f, a.w ? a.offset : 0.f, w[j]);
+        param_pairs(a.b, a.param_f32, c, 0.f, 0.f, b[j]);
+    }
+    const float inv_d = 1.0f / float(a.d);
+    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+    uint16_t* py = a.y + first * a.ld_y + t * 8;
+    int par = 0;
+    int64_t row = first;
+    for (; n > 0; --n, par ^= 1, row += step, py += step * a.ld_y) {
+        cp_async_wait<kS - 2>();
+        uint4 raw[kN];
+        uint64_t f[kN][4];
+        uint64_t sum = 0;
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            raw[j] = lds16(ring.get + j * ring.pitch);
+            const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) { f[j][k] = f2bf16(u[k]); sum = f2add(sum, f[j][k]); }
+        }
+        ring.step(ring.get);
+        issue();
+        float lo, hi, mean = 0.f;
+        if (!a.rms) {
+            f2unpack(sum, lo, hi);
+            mean = group_sum1(lo + hi, &s_x[par][0][g * sh.nw], wg, sh, 1 + g) * inv_d;
+        }
+        uint64_t sq = 0;
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const uint64_t nm = f2splat(in[j] ? -mean : 0.f);
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f[j][k] = f2add(f[j][k], nm);
+                sq = f2fma(f[j][k], f[j][k], sq);
+            }
+        }
+        f2unpack(sq, lo, hi);
+        const float rstd = rsqrtf(group_sum1(lo + hi, &s_x[par][1][g * sh.nw], wg, sh, 1 + g) * inv_d + a.eps);
+        if (t == 0) {
+            if (!a.rms) a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        const uint64_t r2 = f2splat(rstd);
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            if (a.format) {                               // 16 lanes hold a block of 128 columns
+                const int c = (j * gt + t) * 8;
+                const PackFactors pf = pack_factors(absmax_half_warp(absmax8(raw[j])), a.format);
+                if (in[j]) {
+                    *reinterpret_cast<uint2*>(a.q + row * a.d + c) = pack8_codes(raw[j], pf, a.format);
+                    if ((lane & 15) == 0) a.q_scale[row * nb + c / DLM_PACK_BLOCK] = pf.scale;
+                }
+            }
+            if (in[j]) {
+                uint32_t o[4];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = f2to_bf16(f2fma(f2mul(f[j][k], r2), w[j][k], b[j][k]));
+                *reinterpret_cast<uint4*>(py + j * gt * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+    cp_async_wait<0>();
+}
+
+template <int kN, bool kHeld8>
+__global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a, RingShape sh) {
+    constexpr int kS = bwd_stages<kN>();
+    extern __shared__ uint4 ring_mem[];                   // ring of dy, x pieces; at the end [2][d] floats
+    __shared__ float2 s_x[2][16];                         // [row parity][warp]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = warp / sh.nw, wg = warp - g * sh.nw;
+    const int t = wg * 32 + lane, gt = sh.nw * 32;
+    uint64_t w[kN][4], dw[kN][4], db[kN][4];
+    bool in[kN];
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) in[j] = (j * gt + t) * 8 < a.d;
+    Ring<kS, 2 * kN> ring(ring_mem);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
+    int n = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
+    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+    const uint16_t* pdy = a.dy + first * a.ld_dy + t * 8;
+    const uint16_t* px = kHeld8 ? nullptr : a.x + first * a.ld_x + t * 8;
+    const uint8_t* pq = kHeld8 ? a.q + first * a.d + t * 8 : nullptr;
+    int left = n;
+    auto issue = [&]() {
+        if (left > 0) {
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                if (in[j]) {
+                    cp_async16(ring.put + 2 * j * ring.pitch, pdy + j * gt * 8);
+                    if constexpr (kHeld8) cp_async8(ring.put + (2 * j + 1) * ring.pitch, pq + j * gt * 8);
+                    else cp_async16(ring.put + (2 * j + 1) * ring.pitch, px + j * gt * 8);
+                }
+            }
+            pdy += step * a.ld_dy;
+            if constexpr (kHeld8) pq += step * a.d;
+            else px += step * a.ld_x;
+            --left;
+        }
+        cp_async_commit();
+        ring.step(ring.put);
+    };
+    // statistics and block factors of the row after the one in work
+    const float* pmean = a.mean + first;
+    const float* prstd = a.rstd + first;
+    const float* pqs = kHeld8 ? a.q_scale + first * nb : nullptr;
+    float mean_n = 0.f, rstd_n = 0.f, qs_n[kN];
+    auto next_stats = [&](bool more) {
+        if (!more) return;
+        if (!a.rms) mean_n = __ldg(pmean);
+        rstd_n = __ldg(prstd);
+        pmean += step;
+        prstd += step;
+        if constexpr (kHeld8) {
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) qs_n[j] = in[j] ? __ldg(pqs + (j * gt + t) * 8 / DLM_PACK_BLOCK) : 0.f;
+            pqs += step * nb;
+        }
+    };
+    #pragma unroll 1
+    for (int s = 0; s < kS - 1; ++s) issue();
+    next_stats(n > 0);
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        param_pairs(a.w, a.param_f32, in[j] ? (j * gt + t) * 8 : 0, 1.f, a.w ? a.offset : 0.f, w[j]);
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) dw[j][k] = db[j][k] = 0;
+    }
+    const float inv_d = 1.0f / float(a.d);
+    uint16_t* pdx = a.dx + first * a.ld_dx + t * 8;
+    int par = 0;
+    for (; n > 0; --n, par ^= 1, pdx += step * a.ld_dx) {
+        const uint64_t nm = f2splat(-mean_n), r2 = f2splat(rstd_n);
+        uint64_t qs[kN];
+        if constexpr (kHeld8) {
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) qs[j] = f2splat(qs_n[j]);
+        }
+        next_stats(n > 1);
+        cp_async_wait<kS - 2>();
+        uint64_t xh[kN][4], gr[kN][4], s1 = 0, s2 = 0;
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const uint4 y4 = lds16(ring.get + 2 * j * ring.pitch);
+            const uint32_t yw[4] = {y4.x, y4.y, y4.z, y4.w};
+            if constexpr (kHeld8) {
+                const uint2 q2 = lds8(ring.get + (2 * j + 1) * ring.pitch);
+                float v[8];
+                unpack_codes(q2.x, a.format, *reinterpret_cast<float(*)[4]>(v));
+                unpack_codes(q2.y, a.format, *reinterpret_cast<float(*)[4]>(v + 4));
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) xh[j][k] = f2mul(f2pack(v[2 * k], v[2 * k + 1]), qs[j]);
+            } else {
+                const uint4 x4 = lds16(ring.get + (2 * j + 1) * ring.pitch);
+                const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) xh[j][k] = f2bf16(xw[k]);
+            }
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t dy = f2bf16(yw[k]);
+                xh[j][k] = f2mul(f2add(xh[j][k], nm), r2);
+                gr[j][k] = f2mul(dy, w[j][k]);
+                s1 = f2add(s1, gr[j][k]);
+                s2 = f2fma(gr[j][k], xh[j][k], s2);
+                dw[j][k] = f2fma(dy, xh[j][k], dw[j][k]);
+                db[j][k] = f2add(db[j][k], dy);
+            }
+        }
+        ring.step(ring.get);
+        issue();
+        float lo, hi, v1, v2;
+        f2unpack(s1, lo, hi);
+        v1 = lo + hi;
+        f2unpack(s2, lo, hi);
+        v2 = lo + hi;
+        group_sum2(v1, v2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
+        const uint64_t n1 = f2splat(a.rms ? 0.f : -v1 * inv_d), n2 = f2splat(-v2 * inv_d);
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            if (in[j]) {
+                uint32_t o[4];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[k] = f2to_bf16(f2mul(f2add(f2fma(xh[j][k], n2, gr[j][k]), n1), r2));
+                *reinterpret_cast<uint4*>(pdx + j * gt * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+    // the groups' sums, added in the order of the groups
+    cp_async_wait<0>();
+    float* acc = reinterpret_cast<float*>(ring_mem);
+    for (int k = 0; k < sh.groups; ++k) {
+        __syncthreads();
+        if (g != k) continue;
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            if (!in[j]) continue;
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint64_t* p = reinterpret_cast<uint64_t*>(acc + h * a.d + (j * gt + t) * 8);
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t v = h ? db[j][i] : dw[j][i];
+                    p[i] = k ? f2add(p[i], v) : v;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    float* part = a.part + int64_t(blockIdx.x) * 2 * a.pitch;
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+        if (a.want_dw) part[c] = acc[c];
+        if (a.want_db) part[a.pitch + c] = acc[a.d + c];
+    }
+}
+
 // Any width and alignment: a CTA per row, which it reads up to three times
 // (from L2 after the first).
 constexpr int kWideThreads = 512;
@@ -244,62 +595,31 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(NormFwdArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// backward
+// backward by single elements
 // ---------------------------------------------------------------------------
-constexpr int kBwdN = 8;              // elements a lane: one 16-byte piece, or eight 32 * kNW apart
+constexpr int kBwdN = 8;              // elements a lane, 32 * kNW apart
 
-template <int kVec, int kNW>
-__device__ __forceinline__ int bwd_col(int t, int k) {
-    return kVec == 8 ? t * 8 + k : k * kNW * 32 + t;
-}
-
-// x (or its checkpoint's value) and dy of this thread's columns, fp32
-template <int kVec, int kNW>
+// x (or its checkpoint's value) and dy of this thread's columns k * 32 * kNW + t, fp32
+template <int kNW>
 __device__ __forceinline__ void bwd_load(const NormBwdArgs& a, int64_t row, int t, float (&x)[kBwdN], float (&dy)[kBwdN]) {
-    if constexpr (kVec == 8) {
-        const int c = t * 8;
-        #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = dy[k] = 0.f;
-        if (c >= a.d) return;
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.dy + row * a.ld_dy + c));
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        if (a.x) {
-            const uint4 z = __ldg(reinterpret_cast<const uint4*>(a.x + row * a.ld_x + c));
-            const uint32_t w[4] = {z.x, z.y, z.z, z.w};
-            #pragma unroll
-            for (int k = 0; k < 4; ++k) { x[2 * k] = bf16lo(w[k]); x[2 * k + 1] = bf16hi(w[k]); }
-        } else {
-            const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
-            const uint2 z = __ldg(reinterpret_cast<const uint2*>(a.q + row * a.d + c));
-            const float s = __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK);
-            float lo[4], hi[4];
-            unpack_codes(z.x, a.format, lo);
-            unpack_codes(z.y, a.format, hi);
-            #pragma unroll
-            for (int k = 0; k < 4; ++k) { x[k] = lo[k] * s; x[4 + k] = hi[k] * s; }
-        }
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) { dy[2 * k] = bf16lo(u[k]); dy[2 * k + 1] = bf16hi(u[k]); }
-    } else {
-        #pragma unroll
-        for (int k = 0; k < kBwdN; ++k) {
-            const int c = bwd_col<kVec, kNW>(t, k);
-            x[k] = dy[k] = 0.f;
-            if (c < a.d) {
-                dy[k] = bf16_bits_to_float(__ldg(a.dy + row * a.ld_dy + c));
-                if (a.x) {
-                    x[k] = bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c));
-                } else {
-                    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
-                    x[k] = unpack_code(__ldg(a.q + row * a.d + c), a.format) *
-                           __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK);
-                }
+    #pragma unroll
+    for (int k = 0; k < kBwdN; ++k) {
+        const int c = k * kNW * 32 + t;
+        x[k] = dy[k] = 0.f;
+        if (c < a.d) {
+            dy[k] = bf16_bits_to_float(__ldg(a.dy + row * a.ld_dy + c));
+            if (a.x) {
+                x[k] = bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c));
+            } else {
+                const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+                x[k] = unpack_code(__ldg(a.q + row * a.d + c), a.format) *
+                       __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK);
             }
         }
     }
 }
 
-template <int kVec, int kNW>
+template <int kNW>
 __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_bwd(NormBwdArgs a) {
     constexpr int kG = groups_per_cta(kNW);
     constexpr int kR = 2;              // rows at a time: their loads overlap, their sums share a barrier
@@ -312,7 +632,7 @@ __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_bwd(Nor
     pdl_launch_dependents();
     #pragma unroll
     for (int k = 0; k < kBwdN; ++k) {
-        const int c = bwd_col<kVec, kNW>(t, k);
+        const int c = (k * kNW * 32 + t);
         w[k] = c < a.d ? (a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f) : 0.f;
         dw[k] = db[k] = 0.f;
     }
@@ -328,7 +648,7 @@ __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_bwd(Nor
         for (int r = 0; r < kR; ++r) {
             const bool live = r0 + r < a.rows;
             const int64_t row = live ? r0 + r : a.rows - 1;
-            bwd_load<kVec, kNW>(a, row, t, x[r], dy[r]);
+            bwd_load<kNW>(a, row, t, x[r], dy[r]);
             const float mean = a.rms ? 0.f : __ldg(a.mean + row);
             rstd[r] = __ldg(a.rstd + row);
             s1[r] = s2[r] = 0.f;
@@ -338,8 +658,8 @@ __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_bwd(Nor
                 x[r][k] = xh;
                 const float gk = dy[r][k] * w[k];
                 s1[r] += gk;
-                s2[r] += bwd_col<kVec, kNW>(t, k) < a.d ? gk * xh : 0.f;
-                if (live && bwd_col<kVec, kNW>(t, k) < a.d) {
+                s2[r] += (k * kNW * 32 + t) < a.d ? gk * xh : 0.f;
+                if (live && (k * kNW * 32 + t) < a.d) {
                     dw[k] += dy[r][k] * xh;
                     db[k] += dy[r][k];
                 }
@@ -369,23 +689,16 @@ __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_bwd(Nor
             float o[kBwdN];
             #pragma unroll
             for (int k = 0; k < kBwdN; ++k) o[k] = (dy[r][k] * w[k] - m1 - x[r][k] * m2) * rstd[r];
-            if constexpr (kVec == 8) {
-                if (t * 8 < a.d)
-                    *reinterpret_cast<uint4*>(dx + t * 8) =
-                        make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                   pack_bf16x2(o[6], o[7]));
-            } else {
-                #pragma unroll
-                for (int k = 0; k < kBwdN; ++k)
-                    if (bwd_col<kVec, kNW>(t, k) < a.d)
-                        dx[bwd_col<kVec, kNW>(t, k)] = __bfloat16_as_ushort(__float2bfloat16_rn(o[k]));
-            }
+            #pragma unroll
+            for (int k = 0; k < kBwdN; ++k)
+                if ((k * kNW * 32 + t) < a.d)
+                    dx[k * kNW * 32 + t] = __bfloat16_as_ushort(__float2bfloat16_rn(o[k]));
         }
     }
     float* part = a.part + (int64_t(blockIdx.x) * kG + g) * 2 * a.pitch;
     #pragma unroll
     for (int k = 0; k < kBwdN; ++k) {
-        const int c = bwd_col<kVec, kNW>(t, k);
+        const int c = (k * kNW * 32 + t);
         if (c < a.d) {
             if (a.want_dw) part[c] = dw[k];
             if (a.want_db) part[a.pitch + c] = db[k];
@@ -502,27 +815,49 @@ static dlm_status_t launch_fwd_n(int nw, const NormFwdArgs& a, cudaStream_t s) {
     }
 }
 
-template <int kVec, int kNW>
+template <int kNW>
 static dlm_status_t launch_bwd(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
-    return launch_pdl(k_norm_bwd<kVec, kNW>, dim3(grid), dim3(kNW * groups_per_cta(kNW) * 32), 0, s,
-                      "k_norm_bwd launch", a);
+    return launch_pdl(k_norm_bwd<kNW>, dim3(grid), dim3(kNW * groups_per_cta(kNW) * 32), 0, s, "k_norm_bwd launch", a);
 }
 
-template <int kVec>
 static dlm_status_t launch_bwd_n(int nw, const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
     switch (nw) {
-        case 1: return launch_bwd<kVec, 1>(a, grid, s);
-        case 2: return launch_bwd<kVec, 2>(a, grid, s);
-        case 4: return launch_bwd<kVec, 4>(a, grid, s);
-        case 8: return launch_bwd<kVec, 8>(a, grid, s);
-        case 16: return launch_bwd<kVec, 16>(a, grid, s);
-        default: return launch_bwd<kVec, 32>(a, grid, s);
+        case 1: return launch_bwd<1>(a, grid, s);
+        case 2: return launch_bwd<2>(a, grid, s);
+        case 4: return launch_bwd<4>(a, grid, s);
+        case 8: return launch_bwd<8>(a, grid, s);
+        case 16: return launch_bwd<16>(a, grid, s);
+        default: return launch_bwd<32>(a, grid, s);
     }
 }
 
-// How the backward pass splits its rows (by the width alone, so that the
-// workspace does not depend on alignment: the scalar and the vector kernel
-// hold eight elements a lane alike).
+// Ring kernels: one piece a lane up to 256 columns, two beyond, as long as 16
+// warps hold a row; nw = 0: they do not.
+static RingShape ring_shape(int32_t d, int* pieces) {
+    const int nv = (d + 7) / 8;
+    *pieces = nv <= 32 ? 1 : 2;
+    RingShape sh = {(nv + 32 * *pieces - 1) / (32 * *pieces), 0};
+    if (sh.nw > kRingThreads / 32) sh.nw = 0;
+    else sh.groups = kRingThreads / 32 / sh.nw;
+    return sh;
+}
+
+template <typename Args>
+static dlm_status_t launch_ring(void (*kern)(Args, RingShape), const Args& a, RingShape sh, int slots, unsigned grid,
+                                cudaStream_t s, const char* what) {
+    const unsigned threads = unsigned(sh.nw * sh.groups * 32);
+    const size_t smem = size_t(slots) * threads * 16;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               slots * kRingThreads * 16);
+    if (e != cudaSuccess) { cudaGetLastError(); return cuda_status(e, what); }
+    return launch_pdl(kern, dim3(grid), dim3(threads), smem, s, what, a, sh);
+}
+
+static unsigned ring_grid(int64_t rows) { return unsigned(rows < 148 ? rows : 148); }
+
+// How the backward pass splits its rows: `grid` CTAs of the kernels by element
+// (nw warps a row; 0: the wide one).  The workspace holds the partial rows of
+// either these or the ring kernel's, so it does not depend on alignment.
 struct NormBwdPlan { int nw; unsigned grid; int partials; int pitch; size_t bytes; };
 
 static bool norm_bwd_plan(int64_t rows, int32_t d, NormBwdPlan* p) {
@@ -535,7 +870,8 @@ static bool norm_bwd_plan(int64_t rows, int32_t d, NormBwdPlan* p) {
     p->grid = unsigned(need < resident ? need : resident);
     p->partials = int(p->grid) * groups;
     p->pitch = int(align_up(size_t(d), 32));
-    p->bytes = align_up((size_t(p->partials) * 2 + 1) * size_t(p->pitch) * 4, kWsAlign);
+    const int most = p->partials > int(ring_grid(rows)) ? p->partials : int(ring_grid(rows));
+    p->bytes = align_up((size_t(most) * 2 + 1) * size_t(p->pitch) * 4, kWsAlign);
     return true;
 }
 
@@ -567,6 +903,12 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
                      weight_offset, y, ld_y, mean, rstd, pack_format, q, q_scale};
     const bool vec = d_model % 8 == 0 && ld_x % 8 == 0 && ld_y % 8 == 0 && aligned16(x) && aligned16(y) &&
                      param_aligned(weight) && param_aligned(bias) && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
+    int pieces = 0;
+    const RingShape sh = ring_shape(d_model, &pieces);
+    if (vec && sh.nw && rows > 148) {
+        return pieces == 1 ? launch_ring(k_norm_fwd_ring<1>, a, sh, fwd_stages<1>(), ring_grid(rows), s, "k_norm_fwd launch")
+                           : launch_ring(k_norm_fwd_ring<2>, a, sh, 2 * fwd_stages<2>(), ring_grid(rows), s, "k_norm_fwd launch");
+    }
     const int nw = vec ? warps_for(d_model / 8, 4) : warps_for(d_model, 8);
     if (vec && nw) return launch_fwd_n<8, 4>(nw, a, s);
     if (nw) st = launch_fwd_n<1, 8>(nw, a, s);
@@ -613,9 +955,20 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
     if (rows > 0) {
         const bool vec = d_model % 8 == 0 && ld_dy % 8 == 0 && ld_dx % 8 == 0 && aligned16(d_y) && aligned16(d_x) &&
                          (a.x ? ld_x % 8 == 0 && aligned16(x) : (reinterpret_cast<uintptr_t>(q) & 7) == 0);
-        if (!p.nw) st = launch_pdl(k_norm_bwd_wide, dim3(p.grid), dim3(kWideThreads), 0, s, "k_norm_bwd_wide launch", a);
-        else if (vec) st = launch_bwd_n<8>(p.nw, a, p.grid, s);
-        else st = launch_bwd_n<1>(p.nw, a, p.grid, s);
+        int pieces = 0;
+        const RingShape sh = ring_shape(d_model, &pieces);
+        if (vec && sh.nw) {
+            const unsigned grid = ring_grid(rows);
+            p.partials = int(grid);
+            const char* what = "k_norm_bwd launch";
+            if (pieces == 1)
+                st = launch_ring(a.x ? k_norm_bwd_ring<1, false> : k_norm_bwd_ring<1, true>, a, sh,
+                                 2 * bwd_stages<1>(), grid, s, what);
+            else
+                st = launch_ring(a.x ? k_norm_bwd_ring<2, false> : k_norm_bwd_ring<2, true>, a, sh,
+                                 4 * bwd_stages<2>(), grid, s, what);
+        } else if (!p.nw) st = launch_pdl(k_norm_bwd_wide, dim3(p.grid), dim3(kWideThreads), 0, s, "k_norm_bwd_wide launch", a);
+        else st = launch_bwd_n(p.nw, a, p.grid, s);
         if (st != DLM_OK) return st;
     }
     if (!d_weight && !d_bias) return DLM_OK;
