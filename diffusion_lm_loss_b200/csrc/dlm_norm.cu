@@ -67,25 +67,21 @@ __device__ __forceinline__ float param_at(const void* p, int f32, int c) {
     return f32 ? __ldg(static_cast<const float*>(p) + c) : bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(p) + c));
 }
 
-// kVec consecutive parameters from column c on; `none` where there is no array
-template <int kVec>
-__device__ __forceinline__ void load_params(const void* p, int f32, int c, float none, float (&o)[kVec]) {
+// 8 consecutive parameters from column c on, on a 16-byte border; `none` where
+// there is no array
+__device__ __forceinline__ void load_params(const void* p, int f32, int c, float none, float (&o)[8]) {
     if (!p) {
         #pragma unroll
-        for (int k = 0; k < kVec; ++k) o[k] = none;
-    } else if constexpr (kVec == 8) {
-        if (f32) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
-            o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w; o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-        } else {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c));
-            const uint32_t t[4] = {v.x, v.y, v.z, v.w};
-            #pragma unroll
-            for (int k = 0; k < 4; ++k) { o[2 * k] = bf16lo(t[k]); o[2 * k + 1] = bf16hi(t[k]); }
-        }
+        for (int k = 0; k < 8; ++k) o[k] = none;
+    } else if (f32) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w; o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
     } else {
-        o[0] = param_at(p, f32, c);
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c));
+        const uint32_t t[4] = {v.x, v.y, v.z, v.w};
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) { o[2 * k] = bf16lo(t[k]); o[2 * k + 1] = bf16hi(t[k]); }
     }
 }
 
@@ -110,14 +106,23 @@ __device__ __forceinline__ float group_sum(float v, float* slot, int warp_in_gro
     return v;
 }
 
+__device__ __forceinline__ uint64_t f2splat(float v) { return f2pack(v, v); }
+__device__ __forceinline__ uint64_t f2bf16(uint32_t w) { return f2pack(bf16lo(w), bf16hi(w)); }
+
+__device__ __forceinline__ uint32_t f2to_bf16(uint64_t v) {
+    float lo, hi;
+    f2unpack(v, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
+
 // Groups of kNW warps per CTA: at least 4 warps a CTA.
 constexpr int groups_per_cta(int nw) { return nw >= 4 ? 1 : 4 / nw; }
 
 // ---------------------------------------------------------------------------
 // forward: a row in the registers of kNW warps, kN pieces of kVec elements a lane
 // ---------------------------------------------------------------------------
-template <int kVec, int kN, int kNW>
-__global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd(NormFwdArgs a) {
+template <int kN, int kNW>
+__global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd_vec(NormFwdArgs a) {
     constexpr int kG = groups_per_cta(kNW);
     __shared__ float s_x[2][kG][kNW];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -132,72 +137,118 @@ __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd(Nor
     uint4 raw[kN];
     #pragma unroll
     for (int j = 0; j < kN; ++j) {
-        const int c = (j * kNW * 32 + t) * kVec;
-        raw[j] = make_uint4(0, 0, 0, 0);
-        if (c < a.d) {
-            if constexpr (kVec == 8) raw[j] = __ldg(reinterpret_cast<const uint4*>(x + c));
-            else raw[j].x = __ldg(x + c);
-        }
+        const int c = (j * kNW * 32 + t) * 8;
+        raw[j] = c < a.d ? __ldg(reinterpret_cast<const uint4*>(x + c)) : make_uint4(0, 0, 0, 0);
     }
-    float f[kN][kVec];
-    float sum = 0.f;
-    #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-        if constexpr (kVec == 8) {
-            const uint32_t w4[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-            #pragma unroll
-            for (int k = 0; k < 4; ++k) { f[j][2 * k] = bf16lo(w4[k]); f[j][2 * k + 1] = bf16hi(w4[k]); }
-        } else {
-            f[j][0] = bf16_bits_to_float(uint16_t(raw[j].x));
-        }
+    if (a.format) {
+        uint2 code[kN];
+        pack_pieces<kN>(raw, a.format, code, [&](int m, float f) {
+            const int c = (m * kNW * 32 + (t & ~15)) * 8, nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+            if (live && c < a.d) a.q_scale[row * nb + c / DLM_PACK_BLOCK] = f;
+        });
         #pragma unroll
-        for (int k = 0; k < kVec; ++k) sum += f[j][k];
+        for (int j = 0; j < kN; ++j) {
+            const int c = (j * kNW * 32 + t) * 8;
+            if (live && c < a.d) *reinterpret_cast<uint2*>(a.q + row * a.d + c) = code[j];
+        }
     }
     const float inv_d = 1.0f / float(a.d);
-    float mean = 0.f;
-    if (!a.rms) mean = group_sum<kNW>(sum, s_x[0][g], wg) * inv_d;
-    float sq = 0.f;
+    float lo, hi, mean = 0.f;
+    if (!a.rms) {
+        uint64_t sum = 0;
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) sum = f2add(sum, f2bf16(u[k]));
+        }
+        f2unpack(sum, lo, hi);
+        mean = group_sum<kNW>(lo + hi, s_x[0][g], wg) * inv_d;
+    }
+    uint64_t sq = 0;
     #pragma unroll
     for (int j = 0; j < kN; ++j) {
-        const bool in = (j * kNW * 32 + t) * kVec < a.d;
+        const uint64_t nm = f2splat((j * kNW * 32 + t) * 8 < a.d ? -mean : 0.f);
+        const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
         #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            const float v = in ? f[j][k] - mean : 0.f;
-            sq += v * v;
+        for (int k = 0; k < 4; ++k) {
+            const uint64_t v = f2add(f2bf16(u[k]), nm);
+            sq = f2fma(v, v, sq);
         }
     }
-    const float rstd = rsqrtf(group_sum<kNW>(sq, s_x[1][g], wg) * inv_d + a.eps);
+    f2unpack(sq, lo, hi);
+    const float rstd = rsqrtf(group_sum<kNW>(lo + hi, s_x[1][g], wg) * inv_d + a.eps);
     if (live && t == 0) {
         if (!a.rms) a.mean[row] = mean;
         a.rstd[row] = rstd;
     }
     uint16_t* y = a.y + row * a.ld_y;
     const float offset = a.w ? a.offset : 0.f;
+    const uint64_t nm = f2splat(-mean), r2 = f2splat(rstd);
     #pragma unroll
     for (int j = 0; j < kN; ++j) {
-        const int c = (j * kNW * 32 + t) * kVec;
+        const int c = (j * kNW * 32 + t) * 8;
         const bool in = live && c < a.d;
-        if constexpr (kVec == 8) {
-            if (a.format) {                             // 16 lanes hold a block of 128 columns
-                const PackFactors pf = pack_factors(absmax_half_warp(absmax8(raw[j])), a.format);
-                if (in) {
-                    *reinterpret_cast<uint2*>(a.q + row * a.d + c) = pack8_codes(raw[j], pf, a.format);
-                    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
-                    if ((lane & 15) == 0) a.q_scale[row * nb + c / DLM_PACK_BLOCK] = pf.scale;
-                }
+        if (in) {
+            float w[8], b[8];
+            load_params(a.w, a.param_f32, c, 1.f, w);
+            load_params(a.b, a.param_f32, c, 0.f, b);
+            const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+            uint32_t o[4];
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t xh = f2mul(f2add(f2bf16(u[k]), nm), r2);
+                o[k] = f2to_bf16(f2fma(xh, f2pack(w[2 * k] + offset, w[2 * k + 1] + offset), f2pack(b[2 * k], b[2 * k + 1])));
             }
+            *reinterpret_cast<uint4*>(y + c) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if (!in) continue;
-        float w[kVec], b[kVec], o[kVec];
-        load_params<kVec>(a.w, a.param_f32, c, 1.f, w);
-        load_params<kVec>(a.b, a.param_f32, c, 0.f, b);
-        #pragma unroll
-        for (int k = 0; k < kVec; ++k) o[k] = (f[j][k] - mean) * rstd * (w[k] + offset) + b[k];
-        if constexpr (kVec == 8)
-            *reinterpret_cast<uint4*>(y + c) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                                                          pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-        else
-            y[c] = __bfloat16_as_ushort(__float2bfloat16_rn(o[0]));
+    }
+}
+
+// The same by single elements: kN of them a lane, 32 * kNW apart.
+template <int kN, int kNW>
+__global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd(NormFwdArgs a) {
+    constexpr int kG = groups_per_cta(kNW);
+    __shared__ float s_x[2][kG][kNW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = warp / kNW, wg = warp % kNW;
+    const int t = wg * 32 + lane;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t want = int64_t(blockIdx.x) * kG + g;
+    const bool live = want < a.rows;
+    const int64_t row = live ? want : a.rows - 1;
+    const uint16_t* x = a.x + row * a.ld_x;
+    float f[kN], sum = 0.f;
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const int c = j * kNW * 32 + t;
+        f[j] = c < a.d ? bf16_bits_to_float(__ldg(x + c)) : 0.f;
+    }
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) sum += f[j];
+    const float inv_d = 1.0f / float(a.d);
+    const float mean = a.rms ? 0.f : group_sum<kNW>(sum, s_x[0][g], wg) * inv_d;
+    float sq = 0.f;
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        f[j] = j * kNW * 32 + t < a.d ? f[j] - mean : 0.f;
+        sq += f[j] * f[j];
+    }
+    const float rstd = rsqrtf(group_sum<kNW>(sq, s_x[1][g], wg) * inv_d + a.eps);
+    if (!live) return;
+    if (t == 0) {
+        if (!a.rms) a.mean[row] = mean;
+        a.rstd[row] = rstd;
+    }
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const int c = j * kNW * 32 + t;
+        if (c < a.d) {
+            const float w = a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f;
+            const float b = a.b ? param_at(a.b, a.param_f32, c) : 0.f;
+            a.y[row * a.ld_y + c] = __bfloat16_as_ushort(__float2bfloat16_rn(f[j] * rstd * w + b));
+        }
     }
 }
 
@@ -210,7 +261,6 @@ constexpr int kRingThreads = 512;
 // lane, `groups` of them make a CTA.
 struct RingShape { int nw, groups; };
 
-__device__ __forceinline__ uint64_t f2splat(float v) { return f2pack(v, v); }
 
 // The sums of s1 and s2 over a group, in every lane.  Lanes 0..15 carry s1,
 // 16..31 s2.  slot: [nw] float2 that no earlier exchange still reads; `bar`:
@@ -246,14 +296,6 @@ __device__ __forceinline__ float group_sum1(float v, float* slot, int wg, const 
     return v;
 }
 
-__device__ __forceinline__ uint64_t f2bf16(uint32_t w) { return f2pack(bf16lo(w), bf16hi(w)); }
-
-__device__ __forceinline__ uint32_t f2to_bf16(uint64_t v) {
-    float lo, hi;
-    f2unpack(v, lo, hi);
-    return pack_bf16x2(lo, hi);
-}
-
 // 8 parameters as 4 pairs
 __device__ __forceinline__ void param_pairs(const void* p, int f32, int c, float none, float add, uint64_t (&o)[4]) {
     #pragma unroll
@@ -261,8 +303,8 @@ __device__ __forceinline__ void param_pairs(const void* p, int f32, int c, float
         o[k] = p ? f2pack(param_at(p, f32, c + 2 * k) + add, param_at(p, f32, c + 2 * k + 1) + add) : f2splat(none);
 }
 
-template <int kN>
-constexpr int fwd_stages() { return kN == 1 ? 16 : 10; }
+constexpr int kFwdStages = 5;
+constexpr int kFwdThreads = 512;
 template <int kN>
 constexpr int bwd_stages() { return kN == 1 ? 10 : 6; }
 
@@ -294,38 +336,42 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
     return v;
 }
 
-template <int kN>
-__global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a, RingShape sh) {
-    constexpr int kS = fwd_stages<kN>();
+template <int kN, bool kPack>
+__global__ void __launch_bounds__(kFwdThreads, 1) k_norm_fwd_ring(NormFwdArgs a, RingShape sh) {
+    constexpr int kS = kFwdStages, kR = 2;                // two rows at a time: their exchanges share barriers
     extern __shared__ uint4 ring_mem[];
-    __shared__ float s_x[2][2][16];                       // [row parity][sum][warp]
+    __shared__ float2 s_x[2][2][kFwdThreads / 32];        // [turn parity][sum][warp]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = warp / sh.nw, wg = warp - g * sh.nw;
     const int t = wg * 32 + lane, gt = sh.nw * 32;
-    uint64_t w[kN][4], b[kN][4];
     bool in[kN];
     #pragma unroll
     for (int j = 0; j < kN; ++j) in[j] = (j * gt + t) * 8 < a.d;
-    Ring<kS, kN> ring(ring_mem);
+    Ring<kS, kR * kN> ring(ring_mem);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
     int n = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
+    const int64_t dx = step * a.ld_x, dy = step * a.ld_y;
     const uint16_t* px = a.x + first * a.ld_x + t * 8;
     int left = n;
     auto issue = [&]() {
-        if (left > 0) {
-            #pragma unroll
-            for (int j = 0; j < kN; ++j)
-                if (in[j]) cp_async16(ring.put + j * ring.pitch, px + j * gt * 8);
-            px += step * a.ld_x;
-            --left;
+        #pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            if (left > 0) {
+                #pragma unroll
+                for (int j = 0; j < kN; ++j)
+                    if (in[j]) cp_async16(ring.put + (r * kN + j) * ring.pitch, px + j * gt * 8);
+                px += dx;
+                --left;
+            }
         }
         cp_async_commit();
         ring.step(ring.put);
     };
     #pragma unroll 1
     for (int s = 0; s < kS - 1; ++s) issue();
+    uint64_t w[kN][4], b[kN][4];
     #pragma unroll
     for (int j = 0; j < kN; ++j) {
         const int c = in[j] ? (j * gt + t) * 8 : 0;
@@ -337,57 +383,73 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
     uint16_t* py = a.y + first * a.ld_y + t * 8;
     int par = 0;
     int64_t row = first;
-    for (; n > 0; --n, par ^= 1, row += step, py += step * a.ld_y) {
+    for (; n > 0; n -= kR, par ^= 1, row += kR * step, py += kR * dy) {
         cp_async_wait<kS - 2>();
-        uint4 raw[kN];
-        uint64_t f[kN][4];
-        uint64_t sum = 0;
+        uint4 raw[kR][kN];
+        uint64_t f[kR][kN][4];
+        float s1[kR], s2[kR], lo, hi;
         #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            raw[j] = lds16(ring.get + j * ring.pitch);
-            const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+        for (int r = 0; r < kR; ++r) {
+            uint64_t sum = 0;
             #pragma unroll
-            for (int k = 0; k < 4; ++k) { f[j][k] = f2bf16(u[k]); sum = f2add(sum, f[j][k]); }
+            for (int j = 0; j < kN; ++j) {
+                raw[r][j] = lds16(ring.get + (r * kN + j) * ring.pitch);
+                const uint32_t u[4] = {raw[r][j].x, raw[r][j].y, raw[r][j].z, raw[r][j].w};
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) { f[r][j][k] = f2bf16(u[k]); sum = f2add(sum, f[r][j][k]); }
+            }
+            f2unpack(sum, lo, hi);
+            s1[r] = lo + hi;
         }
         ring.step(ring.get);
         issue();
-        float lo, hi, mean = 0.f;
-        if (!a.rms) {
-            f2unpack(sum, lo, hi);
-            mean = group_sum1(lo + hi, &s_x[par][0][g * sh.nw], wg, sh, 1 + g) * inv_d;
-        }
-        uint64_t sq = 0;
-        #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            const uint64_t nm = f2splat(in[j] ? -mean : 0.f);
+        if constexpr (kPack) {
+            uint2 code[kR * kN];
+            pack_pieces<kR * kN>(reinterpret_cast<const uint4(&)[kR * kN]>(raw), a.format, code, [&](int m, float f) {
+                const int r = m / kN, c = ((m % kN) * gt + (t & ~15)) * 8;
+                if (c < a.d && r < n) a.q_scale[(row + r * step) * nb + c / DLM_PACK_BLOCK] = f;
+            });
             #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                f[j][k] = f2add(f[j][k], nm);
-                sq = f2fma(f[j][k], f[j][k], sq);
-            }
+            for (int m = 0; m < kR * kN; ++m)
+                if (in[m % kN] && m / kN < n)
+                    *reinterpret_cast<uint2*>(a.q + (row + (m / kN) * step) * a.d + ((m % kN) * gt + t) * 8) = code[m];
         }
-        f2unpack(sq, lo, hi);
-        const float rstd = rsqrtf(group_sum1(lo + hi, &s_x[par][1][g * sh.nw], wg, sh, 1 + g) * inv_d + a.eps);
-        if (t == 0) {
-            if (!a.rms) a.mean[row] = mean;
-            a.rstd[row] = rstd;
-        }
-        const uint64_t r2 = f2splat(rstd);
+        if (a.rms) s1[0] = s1[1] = 0.f;
+        else group_sum2(s1[0], s1[1], &s_x[par][0][g * sh.nw], wg, sh, 1 + g);
         #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            if (a.format) {                               // 16 lanes hold a block of 128 columns
-                const int c = (j * gt + t) * 8;
-                const PackFactors pf = pack_factors(absmax_half_warp(absmax8(raw[j])), a.format);
-                if (in[j]) {
-                    *reinterpret_cast<uint2*>(a.q + row * a.d + c) = pack8_codes(raw[j], pf, a.format);
-                    if ((lane & 15) == 0) a.q_scale[row * nb + c / DLM_PACK_BLOCK] = pf.scale;
+        for (int r = 0; r < kR; ++r) {
+            s1[r] *= inv_d;                               // the mean
+            uint64_t sq = 0;
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                const uint64_t nm = f2splat(in[j] ? -s1[r] : 0.f);
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[r][j][k] = f2add(f[r][j][k], nm);
+                    sq = f2fma(f[r][j][k], f[r][j][k], sq);
                 }
             }
-            if (in[j]) {
-                uint32_t o[4];
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = f2to_bf16(f2fma(f2mul(f[j][k], r2), w[j][k], b[j][k]));
-                *reinterpret_cast<uint4*>(py + j * gt * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+            f2unpack(sq, lo, hi);
+            s2[r] = lo + hi;
+        }
+        group_sum2(s2[0], s2[1], &s_x[par][1][g * sh.nw], wg, sh, 1 + g);
+        #pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            if (n <= r) break;
+            const float rstd = rsqrtf(s2[r] * inv_d + a.eps);
+            if (t == 0) {
+                if (!a.rms) a.mean[row + r * step] = s1[r];
+                a.rstd[row + r * step] = rstd;
+            }
+            const uint64_t r2 = f2splat(rstd);
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                if (in[j]) {
+                    uint32_t o[4];
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = f2to_bf16(f2fma(f2mul(f[r][j][k], r2), w[j][k], b[j][k]));
+                    *reinterpret_cast<uint4*>(py + r * dy + j * gt * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
         }
     }
@@ -465,10 +527,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     int par = 0;
     for (; n > 0; --n, par ^= 1, pdx += step * a.ld_dx) {
         const uint64_t nm = f2splat(-mean_n), r2 = f2splat(rstd_n);
-        uint64_t qs[kN];
+        float qs[kN];
         if constexpr (kHeld8) {
             #pragma unroll
-            for (int j = 0; j < kN; ++j) qs[j] = f2splat(qs_n[j]);
+            for (int j = 0; j < kN; ++j) qs[j] = qs_n[j];
         }
         next_stats(n > 1);
         cp_async_wait<kS - 2>();
@@ -479,11 +541,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
             const uint32_t yw[4] = {y4.x, y4.y, y4.z, y4.w};
             if constexpr (kHeld8) {
                 const uint2 q2 = lds8(ring.get + (2 * j + 1) * ring.pitch);
-                float v[8];
-                unpack_codes(q2.x, a.format, *reinterpret_cast<float(*)[4]>(v));
-                unpack_codes(q2.y, a.format, *reinterpret_cast<float(*)[4]>(v + 4));
+                unpack_codes(q2.x, a.format, xh[j][0], xh[j][1]);
+                unpack_codes(q2.y, a.format, xh[j][2], xh[j][3]);
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) xh[j][k] = f2mul(f2pack(v[2 * k], v[2 * k + 1]), qs[j]);
+                for (int k = 0; k < 4; ++k) xh[j][k] = f2mul_rounded(xh[j][k], qs[j]);
             } else {
                 const uint4 x4 = lds16(ring.get + (2 * j + 1) * ring.pitch);
                 const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
@@ -788,11 +849,10 @@ static bool finite_f(float v) { return v - v == 0.0f; }
 
 static bool param_aligned(const void* p) { return !p || aligned16(p); }
 
-template <int kVec, int kN, int kNW>
-static dlm_status_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
+template <int kNW>
+static dlm_status_t launch_fwd(void (*kern)(NormFwdArgs), const NormFwdArgs& a, cudaStream_t s) {
     constexpr int kG = groups_per_cta(kNW);
-    return launch_pdl(k_norm_fwd<kVec, kN, kNW>, dim3(unsigned((a.rows + kG - 1) / kG)), dim3(kNW * kG * 32), 0, s,
-                      "k_norm_fwd launch", a);
+    return launch_pdl(kern, dim3(unsigned((a.rows + kG - 1) / kG)), dim3(kNW * kG * 32), 0, s, "k_norm_fwd launch", a);
 }
 
 // warps that a row of `pieces` pieces takes at `per` pieces a lane: a power of
@@ -803,15 +863,26 @@ static int warps_for(int64_t pieces, int per) {
     return 0;
 }
 
-template <int kVec, int kN>
-static dlm_status_t launch_fwd_n(int nw, const NormFwdArgs& a, cudaStream_t s) {
+template <int kN>
+static dlm_status_t launch_fwd_vec(int nw, const NormFwdArgs& a, cudaStream_t s) {
     switch (nw) {
-        case 1: return launch_fwd<kVec, kN, 1>(a, s);
-        case 2: return launch_fwd<kVec, kN, 2>(a, s);
-        case 4: return launch_fwd<kVec, kN, 4>(a, s);
-        case 8: return launch_fwd<kVec, kN, 8>(a, s);
-        case 16: return launch_fwd<kVec, kN, 16>(a, s);
-        default: return launch_fwd<kVec, kN, 32>(a, s);
+        case 1: return launch_fwd<1>(k_norm_fwd_vec<kN, 1>, a, s);
+        case 2: return launch_fwd<2>(k_norm_fwd_vec<kN, 2>, a, s);
+        case 4: return launch_fwd<4>(k_norm_fwd_vec<kN, 4>, a, s);
+        case 8: return launch_fwd<8>(k_norm_fwd_vec<kN, 8>, a, s);
+        case 16: return launch_fwd<16>(k_norm_fwd_vec<kN, 16>, a, s);
+        default: return launch_fwd<32>(k_norm_fwd_vec<kN, 32>, a, s);
+    }
+}
+
+static dlm_status_t launch_fwd_any(int nw, const NormFwdArgs& a, cudaStream_t s) {
+    switch (nw) {
+        case 1: return launch_fwd<1>(k_norm_fwd<8, 1>, a, s);
+        case 2: return launch_fwd<2>(k_norm_fwd<8, 2>, a, s);
+        case 4: return launch_fwd<4>(k_norm_fwd<8, 4>, a, s);
+        case 8: return launch_fwd<8>(k_norm_fwd<8, 8>, a, s);
+        case 16: return launch_fwd<16>(k_norm_fwd<8, 16>, a, s);
+        default: return launch_fwd<32>(k_norm_fwd<8, 32>, a, s);
     }
 }
 
@@ -833,22 +904,21 @@ static dlm_status_t launch_bwd_n(int nw, const NormBwdArgs& a, unsigned grid, cu
 
 // Ring kernels: one piece a lane up to 256 columns, two beyond, as long as 16
 // warps hold a row; nw = 0: they do not.
-static RingShape ring_shape(int32_t d, int* pieces) {
+static RingShape ring_shape(int32_t d, int warps, int* pieces) {
     const int nv = (d + 7) / 8;
     *pieces = nv <= 32 ? 1 : 2;
     RingShape sh = {(nv + 32 * *pieces - 1) / (32 * *pieces), 0};
-    if (sh.nw > kRingThreads / 32) sh.nw = 0;
-    else sh.groups = kRingThreads / 32 / sh.nw;
+    if (sh.nw > 16) sh.nw = 0;
+    else sh.groups = warps / sh.nw < 15 || sh.nw == 1 ? warps / sh.nw : 15;   // a barrier for each
     return sh;
 }
 
 template <typename Args>
-static dlm_status_t launch_ring(void (*kern)(Args, RingShape), const Args& a, RingShape sh, int slots, unsigned grid,
-                                cudaStream_t s, const char* what) {
+static dlm_status_t launch_ring(void (*kern)(Args, RingShape), const Args& a, RingShape sh, int slots, size_t more,
+                                unsigned grid, cudaStream_t s, const char* what) {
     const unsigned threads = unsigned(sh.nw * sh.groups * 32);
-    const size_t smem = size_t(slots) * threads * 16;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               slots * kRingThreads * 16);
+    const size_t smem = size_t(slots) * threads * 16 + more;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) { cudaGetLastError(); return cuda_status(e, what); }
     return launch_pdl(kern, dim3(grid), dim3(threads), smem, s, what, a, sh);
 }
@@ -861,7 +931,7 @@ static unsigned ring_grid(int64_t rows) { return unsigned(rows < 148 ? rows : 14
 struct NormBwdPlan { int nw; unsigned grid; int partials; int pitch; size_t bytes; };
 
 static bool norm_bwd_plan(int64_t rows, int32_t d, NormBwdPlan* p) {
-    if (rows < 0 || d < 1 || d > INT32_MAX - 128) return false;
+    if (rows < 0 || d < 1 || d > INT32_MAX - 1024) return false;
     p->nw = warps_for(d, kBwdN);
     const int groups = p->nw ? groups_per_cta(p->nw) : 1;
     const int threads = p->nw ? p->nw * groups * 32 : kWideThreads;
@@ -885,7 +955,7 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
                                      float* rstd, int32_t pack_format, uint8_t* q, float* q_scale,
                                      dlm_stream_t stream) {
     DLM_NVTX("dlm_norm_fwd");
-    if (rows < 0 || d_model < 1 || d_model > INT32_MAX - 128 || ld_x < d_model || ld_y < d_model)
+    if (rows < 0 || d_model < 1 || d_model > INT32_MAX - 1024 || ld_x < d_model || ld_y < d_model)
         return DLM_ERR_INVALID_ARGUMENT;
     if (kind != DLM_NORM_LAYER && kind != DLM_NORM_RMS) return DLM_ERR_INVALID_ARGUMENT;
     if (param_dtype != DLM_BF16 && param_dtype != DLM_F32) return DLM_ERR_INVALID_ARGUMENT;
@@ -904,14 +974,15 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
     const bool vec = d_model % 8 == 0 && ld_x % 8 == 0 && ld_y % 8 == 0 && aligned16(x) && aligned16(y) &&
                      param_aligned(weight) && param_aligned(bias) && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
     int pieces = 0;
-    const RingShape sh = ring_shape(d_model, &pieces);
-    if (vec && sh.nw && rows > 148) {
-        return pieces == 1 ? launch_ring(k_norm_fwd_ring<1>, a, sh, fwd_stages<1>(), ring_grid(rows), s, "k_norm_fwd launch")
-                           : launch_ring(k_norm_fwd_ring<2>, a, sh, 2 * fwd_stages<2>(), ring_grid(rows), s, "k_norm_fwd launch");
+    const RingShape sh = ring_shape(d_model, kFwdThreads / 32, &pieces);
+    if (vec && sh.nw && d_model <= 8192 && rows > 148) {
+        auto kern = pieces == 1 ? (pack_format ? k_norm_fwd_ring<1, true> : k_norm_fwd_ring<1, false>)
+                                : (pack_format ? k_norm_fwd_ring<2, true> : k_norm_fwd_ring<2, false>);
+        return launch_ring(kern, a, sh, 2 * pieces * kFwdStages, 0, ring_grid(rows), s, "k_norm_fwd launch");
     }
     const int nw = vec ? warps_for(d_model / 8, 4) : warps_for(d_model, 8);
-    if (vec && nw) return launch_fwd_n<8, 4>(nw, a, s);
-    if (nw) st = launch_fwd_n<1, 8>(nw, a, s);
+    if (vec && nw) return launch_fwd_vec<4>(nw, a, s);
+    if (nw) st = launch_fwd_any(nw, a, s);
     else st = launch_pdl(k_norm_fwd_wide, dim3(unsigned(rows < 148 * 4 ? rows : 148 * 4)), dim3(kWideThreads), 0, s,
                          "k_norm_fwd_wide launch", a);
     if (st != DLM_OK || pack_format == DLM_PACK_NONE) return st;
@@ -956,17 +1027,17 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
         const bool vec = d_model % 8 == 0 && ld_dy % 8 == 0 && ld_dx % 8 == 0 && aligned16(d_y) && aligned16(d_x) &&
                          (a.x ? ld_x % 8 == 0 && aligned16(x) : (reinterpret_cast<uintptr_t>(q) & 7) == 0);
         int pieces = 0;
-        const RingShape sh = ring_shape(d_model, &pieces);
+        const RingShape sh = ring_shape(d_model, kRingThreads / 32, &pieces);
         if (vec && sh.nw) {
             const unsigned grid = ring_grid(rows);
             p.partials = int(grid);
             const char* what = "k_norm_bwd launch";
             if (pieces == 1)
                 st = launch_ring(a.x ? k_norm_bwd_ring<1, false> : k_norm_bwd_ring<1, true>, a, sh,
-                                 2 * bwd_stages<1>(), grid, s, what);
+                                 2 * bwd_stages<1>(), 0, grid, s, what);
             else
                 st = launch_ring(a.x ? k_norm_bwd_ring<2, false> : k_norm_bwd_ring<2, true>, a, sh,
-                                 4 * bwd_stages<2>(), grid, s, what);
+                                 4 * bwd_stages<2>(), 0, grid, s, what);
         } else if (!p.nw) st = launch_pdl(k_norm_bwd_wide, dim3(p.grid), dim3(kWideThreads), 0, s, "k_norm_bwd_wide launch", a);
         else st = launch_bwd_n(p.nw, a, p.grid, s);
         if (st != DLM_OK) return st;

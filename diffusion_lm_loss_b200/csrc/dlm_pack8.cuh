@@ -28,27 +28,11 @@ __device__ __forceinline__ PackFactors pack_factors(float amax, int format) {
     return f;
 }
 
-// Code of one element.  inv = 0 (a block held as zeros or NaN) gives code 0
-// whatever x is: the caller passes 0 for x there.
+// Code of one element (x = 0 where the block is not finite).
 __device__ __forceinline__ uint32_t pack_code(float x, float inv, int format) {
     const float u = __fmul_rn(x, inv);
     if (format == DLM_PACK_INT8) return uint32_t(__float2int_rn(u)) & 0xffu;
     return uint32_t(__nv_cvt_float_to_fp8(u, __NV_SATFINITE, __NV_E4M3));
-}
-
-// Four codes (as consecutive bytes) back to fp32, before the scale.
-__device__ __forceinline__ void unpack_codes(uint32_t w, int format, float (&v)[4]) {
-    if (format == DLM_PACK_INT8) {
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = float(int(w << (24 - 8 * k)) >> 24);
-    } else {
-        #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> (16 * k)), __NV_E4M3);
-            const float2 f = __half22float2(__half2(h));
-            v[2 * k] = f.x; v[2 * k + 1] = f.y;
-        }
-    }
 }
 
 __device__ __forceinline__ float unpack_code(uint8_t c, int format) {
@@ -56,33 +40,83 @@ __device__ __forceinline__ float unpack_code(uint8_t c, int format) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_fp8_storage_t(c), __NV_E4M3)));
 }
 
-// max |.| of 8 bf16 as fp32; a NaN among them comes back as NaN.
-__device__ __forceinline__ float absmax8(uint4 r) {
+// Four codes (consecutive bytes) back to two fp32 pairs, before the scale.
+// An integer code c goes into the fraction of 2^23 as c + 128: one byte
+// permutation per code and one packed subtraction per pair, where int -> float
+// conversions run at a quarter of that rate.
+__device__ __forceinline__ void unpack_codes(uint32_t w, int format, uint64_t& lo, uint64_t& hi) {
+    if (format == DLM_PACK_INT8) {
+        w ^= 0x80808080u;
+        auto at = [&](uint32_t sel) { return __uint_as_float(__byte_perm(w, 0x4b000000u, sel)); };
+        const uint64_t off = f2pack(-8388736.f, -8388736.f);      // -(2^23 + 128)
+        lo = f2add(f2pack(at(0x7440), at(0x7441)), off);
+        hi = f2add(f2pack(at(0x7442), at(0x7443)), off);
+    } else {
+        const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w), __NV_E4M3)));
+        const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> 16), __NV_E4M3)));
+        lo = f2pack(a.x, a.y);
+        hi = f2pack(b.x, b.y);
+    }
+}
+
+// max |.| of 8 bf16, as the bits of an fp32 value; those of a NaN if there is
+// one (non-negative patterns order like their values, NaN above infinity).
+__device__ __forceinline__ uint32_t absmax8(uint4 r) {
     auto b = [](uint32_t w) { w &= 0x7fff7fffu; return *reinterpret_cast<__nv_bfloat162*>(&w); };
     const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(b(r.x), b(r.y)), __hmax2_nan(b(r.z), b(r.w)));
     const uint32_t w = *reinterpret_cast<const uint32_t*>(&m) & 0x7fff7fffu;
-    // non-negative patterns order like their values, NaN above infinity
-    return __uint_as_float(max(w << 16, w & 0xffff0000u));
+    return max(w << 16, w & 0xffff0000u);
 }
 
-// max of non-negative floats (or NaN) over groups of 16 lanes
-__device__ __forceinline__ float absmax_half_warp(float a) {
-    uint32_t u = __float_as_uint(a);
+// Packs M pieces of 8 bf16, each of 16 neighbouring lanes' m-th piece making a
+// block: out[m] gets the lane's 8 codes; put(m, scale) is called by some
+// lane of the 16 for each m.  The M maxima share their exchanges (each halving of
+// the lanes also halves the blocks a lane carries on), and every lane divides
+// for one block only.
+template <int M, typename Put>
+__device__ __forceinline__ void pack_pieces(const uint4 (&r)[M], int format, uint2 (&out)[M], Put&& put) {
+    static_assert(M == 1 || M == 2 || M == 4, "pieces");
+    const int lane = threadIdx.x & 31;
+    uint32_t a[M];
     #pragma unroll
-    for (int o = 8; o; o >>= 1) u = max(u, __shfl_xor_sync(~0u, u, o));
-    return __uint_as_float(u);
-}
-
-// Codes of 8 bf16 with the block's factors: 8 bytes.
-__device__ __forceinline__ uint2 pack8_codes(uint4 r, PackFactors f, int format) {
-    const uint32_t x[4] = {r.x, r.y, r.z, r.w};
-    uint32_t c[4];
+    for (int m = 0; m < M; ++m) a[m] = absmax8(r[m]);
+    int mine = 0, bit = 8;
     #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float lo = f.inv != 0.f ? bf16lo(x[k]) : 0.f, hi = f.inv != 0.f ? bf16hi(x[k]) : 0.f;
-        c[k] = pack_code(lo, f.inv, format) | pack_code(hi, f.inv, format) << 8;
+    for (int h = M / 2; h; h >>= 1, bit >>= 1) {
+        const bool up = lane & bit;
+        #pragma unroll
+        for (int k = 0; k < h; ++k) {
+            const uint32_t keep = up ? a[k + h] : a[k], send = up ? a[k] : a[k + h];
+            a[k] = max(keep, __shfl_xor_sync(~0u, send, bit));
+        }
+        mine = 2 * mine + up;
     }
-    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    #pragma unroll
+    for (; bit; bit >>= 1) a[0] = max(a[0], __shfl_xor_sync(~0u, a[0], bit));
+    const PackFactors f = pack_factors(__uint_as_float(a[0]), format);
+    if ((lane & (16 / M - 1)) == 0) put(mine, f.scale);
+    #pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const float inv = M == 1 ? f.inv : __shfl_sync(~0u, f.inv, (lane & 16) | m * (16 / M));
+        const bool none = inv == 0.f;               // zeros, or a block that is not finite
+        const uint32_t x[4] = {none ? 0u : r[m].x, none ? 0u : r[m].y, none ? 0u : r[m].z, none ? 0u : r[m].w};
+        uint32_t c[4];
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint64_t u = f2mul_rounded(f2pack(bf16lo(x[k]), bf16hi(x[k])), inv);
+            float lo, hi;
+            if (format == DLM_PACK_INT8) {
+                // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits
+                u = f2add(u, f2pack(12582912.f, 12582912.f));
+                f2unpack(u, lo, hi);
+                c[k] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
+            } else {
+                f2unpack(u, lo, hi);
+                c[k] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+            }
+        }
+        out[m] = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+    }
 }
 
 }  // namespace dlm
