@@ -77,17 +77,22 @@ __device__ __forceinline__ uint64_t f2add(uint64_t a, uint64_t b) {
     return d;
 }
 // The compiler may still merge this product with a packed addition after it
-// into one FMA (measured: codes of dlm_pack8 a step off at ties); f2mul_rounded
-// is for products whose own rounding counts.
+// into one FMA (measured: codes of dlm_pack8 a step off at ties).  Where the
+// product's own rounding counts, f2mul_rounded adds a -0 that the compiler
+// cannot tell from another number: that changes no value, zeros of either sign
+// included, and an FMA's result is not merged again.  A constant -0 is seen
+// through (measured), so the -0 is made from a small number known at run time.
 __device__ __forceinline__ uint64_t f2mul(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t f2mul_rounded(uint64_t a, float b) {
-    float lo, hi;
-    f2unpack(a, lo, hi);
-    return f2pack(__fmul_rn(lo, b), __fmul_rn(hi, b));
+__device__ __forceinline__ uint64_t f2negative_zero(int below_256) {
+    const float z = __uint_as_float(0x80000000u | (uint32_t(below_256) >> 8));
+    return f2pack(z, z);
+}
+__device__ __forceinline__ uint64_t f2mul_rounded(uint64_t a, uint64_t b, uint64_t negative_zero) {
+    return f2fma(a, b, negative_zero);
 }
 
 // ---------------------------------------------------------------------------

@@ -388,8 +388,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_embed_join(EmbGradArgs a) {
             const int k0 = min(cnt, warp * per), k1 = min(cnt, k0 + per);
             float acc = 0.f;
             if (col < a.d) {
-                #pragma unroll 8
-                for (int k = k0; k < k1; ++k) acc += a.part[((f + k) * 2 + (k == 0)) * int64_t(a.pitch) + col];
+                constexpr int kU = 8;      // loads in flight
+                for (int k = k0; k < k1; k += kU) {
+                    float x[kU];
+                    #pragma unroll
+                    for (int u = 0; u < kU; ++u)
+                        x[u] = k + u < k1 ? a.part[((f + k + u) * 2 + (k + u == 0)) * int64_t(a.pitch) + col] : 0.f;
+                    #pragma unroll
+                    for (int u = 0; u < kU; ++u) acc += x[u];
+                }
             }
             s[warp][lane] = acc;
             __syncthreads();

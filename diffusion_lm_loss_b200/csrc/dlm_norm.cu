@@ -298,18 +298,33 @@ __device__ __forceinline__ float group_sum1(float v, float* slot, int wg, const 
 
 // 8 parameters as 4 pairs
 __device__ __forceinline__ void param_pairs(const void* p, int f32, int c, float none, float add, uint64_t (&o)[4]) {
+    float v[8];
+    if (!p || (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        load_params(p, f32, c, none, v);
+    } else {
+        #pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = param_at(p, f32, c + k);
+    }
     #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        o[k] = p ? f2pack(param_at(p, f32, c + 2 * k) + add, param_at(p, f32, c + 2 * k + 1) + add) : f2splat(none);
+    for (int k = 0; k < 4; ++k) o[k] = f2pack(v[2 * k] + add, v[2 * k + 1] + add);
 }
 
 constexpr int kFwdStages = 5;
-constexpr int kFwdThreads = 512;
+// Which forward kernel, by the call's 16-byte pieces (rows x d / 8).  The fewer,
+// the more warps share a row, so that one row's time, not the bandwidth,
+// counts less; the ring pays once its start is spread over enough rows.
+// Measured (us), d = 4,096, one / two / four pieces a lane / ring:
+//   148 rows 2.5 / 2.9 / 3.6 / 4.4   600 rows 4.8 / 3.8 / 4.5 / 5.0
+//   1,000 rows 6.5 / 5.7 / 4.7 / 5.6   16,384 rows - / - / 52.0 / 47.1
+// and at d = 1,024: 1,000 rows 2.9 / 3.0 / 3.7, 6,144 rows - / - / 7.3 / 6.8.
+// With the checkpoint written too the ring is not faster (67.2 against 65.4 at
+// 16,384 x 4,096) and is not built.
+constexpr int64_t kOnePiece = 148 * 1024, kTwoPieces = 148 * 2560, kRingPieces = 148 * 4608;
 template <int kN>
 constexpr int bwd_stages() { return kN == 1 ? 10 : 6; }
 
 // A thread's slots of the ring, [stages][pieces] of 16 bytes, the threads side
-// by side.  `in`: the pieces that lie inside the row; the others stay zero.
+// by side.  Pieces that lie outside the row are never copied and stay zero.
 template <int kS, int kPieces>
 struct Ring {
     uint32_t base, pitch, put, get;
@@ -317,7 +332,10 @@ struct Ring {
         base = smem_addr(smem + threadIdx.x);
         pitch = blockDim.x * 16u;
         put = get = base;
-        for (int k = 0; k < kS * kPieces; ++k) smem[threadIdx.x + k * blockDim.x] = make_uint4(0, 0, 0, 0);
+    }
+    // zeros for good in one piece's slots
+    __device__ __forceinline__ void clear(uint4* smem, int piece) const {
+        for (int k = piece; k < kS * kPieces; k += kPieces) smem[threadIdx.x + k * blockDim.x] = make_uint4(0, 0, 0, 0);
     }
     __device__ __forceinline__ void step(uint32_t& at) const {
         at += kPieces * pitch;
@@ -336,11 +354,11 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
     return v;
 }
 
-template <int kN, bool kPack>
-__global__ void __launch_bounds__(kFwdThreads, 1) k_norm_fwd_ring(NormFwdArgs a, RingShape sh) {
+template <int kN>
+__global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a, RingShape sh) {
     constexpr int kS = kFwdStages, kR = 2;                // two rows at a time: their exchanges share barriers
     extern __shared__ uint4 ring_mem[];
-    __shared__ float2 s_x[2][2][kFwdThreads / 32];        // [turn parity][sum][warp]
+    __shared__ float2 s_x[2][2][kRingThreads / 32];        // [turn parity][sum][warp]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = warp / sh.nw, wg = warp - g * sh.nw;
     const int t = wg * 32 + lane, gt = sh.nw * 32;
@@ -348,6 +366,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_fwd_ring(NormFwdArgs a,
     #pragma unroll
     for (int j = 0; j < kN; ++j) in[j] = (j * gt + t) * 8 < a.d;
     Ring<kS, kR * kN> ring(ring_mem);
+    #pragma unroll
+    for (int j = 0; j < kR * kN; ++j)
+        if (!in[j % kN]) ring.clear(ring_mem, j);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
@@ -379,13 +400,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_fwd_ring(NormFwdArgs a,
         param_pairs(a.b, a.param_f32, c, 0.f, 0.f, b[j]);
     }
     const float inv_d = 1.0f / float(a.d);
-    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
     uint16_t* py = a.y + first * a.ld_y + t * 8;
     int par = 0;
     int64_t row = first;
     for (; n > 0; n -= kR, par ^= 1, row += kR * step, py += kR * dy) {
         cp_async_wait<kS - 2>();
-        uint4 raw[kR][kN];
         uint64_t f[kR][kN][4];
         float s1[kR], s2[kR], lo, hi;
         #pragma unroll
@@ -393,8 +412,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_fwd_ring(NormFwdArgs a,
             uint64_t sum = 0;
             #pragma unroll
             for (int j = 0; j < kN; ++j) {
-                raw[r][j] = lds16(ring.get + (r * kN + j) * ring.pitch);
-                const uint32_t u[4] = {raw[r][j].x, raw[r][j].y, raw[r][j].z, raw[r][j].w};
+                const uint4 raw = lds16(ring.get + (r * kN + j) * ring.pitch);
+                const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) { f[r][j][k] = f2bf16(u[k]); sum = f2add(sum, f[r][j][k]); }
             }
@@ -403,17 +422,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_fwd_ring(NormFwdArgs a,
         }
         ring.step(ring.get);
         issue();
-        if constexpr (kPack) {
-            uint2 code[kR * kN];
-            pack_pieces<kR * kN>(reinterpret_cast<const uint4(&)[kR * kN]>(raw), a.format, code, [&](int m, float f) {
-                const int r = m / kN, c = ((m % kN) * gt + (t & ~15)) * 8;
-                if (c < a.d && r < n) a.q_scale[(row + r * step) * nb + c / DLM_PACK_BLOCK] = f;
-            });
-            #pragma unroll
-            for (int m = 0; m < kR * kN; ++m)
-                if (in[m % kN] && m / kN < n)
-                    *reinterpret_cast<uint2*>(a.q + (row + (m / kN) * step) * a.d + ((m % kN) * gt + t) * 8) = code[m];
-        }
         if (a.rms) s1[0] = s1[1] = 0.f;
         else group_sum2(s1[0], s1[1], &s_x[par][0][g * sh.nw], wg, sh, 1 + g);
         #pragma unroll
@@ -456,9 +464,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_fwd_ring(NormFwdArgs a,
     cp_async_wait<0>();
 }
 
-template <int kN, bool kHeld8>
+// kFormat: DLM_PACK_NONE (x itself) or the format of its checkpoint
+template <int kN, int kFormat>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a, RingShape sh) {
     constexpr int kS = bwd_stages<kN>();
+    constexpr bool kHeld8 = kFormat != DLM_PACK_NONE;
     extern __shared__ uint4 ring_mem[];                   // ring of dy, x pieces; at the end [2][d] floats
     __shared__ float2 s_x[2][16];                         // [row parity][warp]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -469,6 +479,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     #pragma unroll
     for (int j = 0; j < kN; ++j) in[j] = (j * gt + t) * 8 < a.d;
     Ring<kS, 2 * kN> ring(ring_mem);
+    #pragma unroll
+    for (int j = 0; j < 2 * kN; ++j)
+        if (!in[j / 2]) ring.clear(ring_mem, j);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
@@ -541,20 +554,21 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
             const uint32_t yw[4] = {y4.x, y4.y, y4.z, y4.w};
             if constexpr (kHeld8) {
                 const uint2 q2 = lds8(ring.get + (2 * j + 1) * ring.pitch);
-                unpack_codes(q2.x, a.format, xh[j][0], xh[j][1]);
-                unpack_codes(q2.y, a.format, xh[j][2], xh[j][3]);
+                unpack_codes(q2.x, kFormat, xh[j][0], xh[j][1]);
+                unpack_codes(q2.y, kFormat, xh[j][2], xh[j][3]);
+                // code * scale - mean in one FMA: the held value is not rounded
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) xh[j][k] = f2mul_rounded(xh[j][k], qs[j]);
+                for (int k = 0; k < 4; ++k) xh[j][k] = f2fma(xh[j][k], f2splat(qs[j]), nm);
             } else {
                 const uint4 x4 = lds16(ring.get + (2 * j + 1) * ring.pitch);
                 const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) xh[j][k] = f2bf16(xw[k]);
+                for (int k = 0; k < 4; ++k) xh[j][k] = f2add(f2bf16(xw[k]), nm);
             }
             #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint64_t dy = f2bf16(yw[k]);
-                xh[j][k] = f2mul(f2add(xh[j][k], nm), r2);
+                xh[j][k] = f2mul(xh[j][k], r2);
                 gr[j][k] = f2mul(dy, w[j][k]);
                 s1 = f2add(s1, gr[j][k]);
                 s2 = f2fma(gr[j][k], xh[j][k], s2);
@@ -660,9 +674,10 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(NormFwdArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kBwdN = 8;              // elements a lane, 32 * kNW apart
 
-// x (or its checkpoint's value) and dy of this thread's columns k * 32 * kNW + t, fp32
+// x - mean (x: or its checkpoint's value) and dy of this thread's columns k * 32 * kNW + t, fp32
 template <int kNW>
-__device__ __forceinline__ void bwd_load(const NormBwdArgs& a, int64_t row, int t, float (&x)[kBwdN], float (&dy)[kBwdN]) {
+__device__ __forceinline__ void bwd_load(const NormBwdArgs& a, int64_t row, int t, float mean, float (&x)[kBwdN],
+                                         float (&dy)[kBwdN]) {
     #pragma unroll
     for (int k = 0; k < kBwdN; ++k) {
         const int c = k * kNW * 32 + t;
@@ -670,11 +685,11 @@ __device__ __forceinline__ void bwd_load(const NormBwdArgs& a, int64_t row, int 
         if (c < a.d) {
             dy[k] = bf16_bits_to_float(__ldg(a.dy + row * a.ld_dy + c));
             if (a.x) {
-                x[k] = bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c));
+                x[k] = bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c)) - mean;
             } else {
                 const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
-                x[k] = unpack_code(__ldg(a.q + row * a.d + c), a.format) *
-                       __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK);
+                x[k] = fmaf(unpack_code(__ldg(a.q + row * a.d + c), a.format),
+                            __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK), -mean);
             }
         }
     }
@@ -709,13 +724,13 @@ __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_bwd(Nor
         for (int r = 0; r < kR; ++r) {
             const bool live = r0 + r < a.rows;
             const int64_t row = live ? r0 + r : a.rows - 1;
-            bwd_load<kNW>(a, row, t, x[r], dy[r]);
             const float mean = a.rms ? 0.f : __ldg(a.mean + row);
+            bwd_load<kNW>(a, row, t, mean, x[r], dy[r]);
             rstd[r] = __ldg(a.rstd + row);
             s1[r] = s2[r] = 0.f;
             #pragma unroll
             for (int k = 0; k < kBwdN; ++k) {
-                const float xh = (x[r][k] - mean) * rstd[r];
+                const float xh = x[r][k] * rstd[r];
                 x[r][k] = xh;
                 const float gk = dy[r][k] * w[k];
                 s1[r] += gk;
@@ -780,10 +795,10 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_bwd_wide(NormBwdArgs a) {
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false) {
         const float mean = a.rms ? 0.f : a.mean[row], rstd = a.rstd[row];
         auto xh_at = [&](int c) {
-            const float x = a.x ? bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c))
-                                : unpack_code(__ldg(a.q + row * a.d + c), a.format) *
-                                      __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK);
-            return (x - mean) * rstd;
+            const float x = a.x ? bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c)) - mean
+                                : fmaf(unpack_code(__ldg(a.q + row * a.d + c), a.format),
+                                       __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK), -mean);
+            return x * rstd;
         };
         float s1 = 0.f, s2 = 0.f;
         for (int c = threadIdx.x; c < a.d; c += kWideThreads) {
@@ -807,7 +822,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_bwd_wide(NormBwdArgs a) {
 
 // dw (blockIdx.y = 0) and db (1) from the partial rows: a lane per column, the
 // warps take consecutive parts of the rows.
-constexpr int kNormJoinWarps = 8;
+constexpr int kNormJoinWarps = 16;
 
 __global__ void __launch_bounds__(kNormJoinWarps * 32) k_norm_join(const float* __restrict__ part, int n_part,
                                                                    int pitch, int d, int grad_f32, int accumulate,
@@ -824,8 +839,14 @@ __global__ void __launch_bounds__(kNormJoinWarps * 32) k_norm_join(const float* 
     float acc = 0.f;
     if (c < d) {
         const float* p = part + blockIdx.y * pitch + c;
-        #pragma unroll 8
-        for (int k = k0; k < k1; ++k) acc += p[int64_t(k) * 2 * pitch];
+        constexpr int kU = 10;         // loads in flight: 148 partial rows are one batch for each warp
+        for (int k = k0; k < k1; k += kU) {
+            float v[kU];
+            #pragma unroll
+            for (int u = 0; u < kU; ++u) v[u] = k + u < k1 ? p[int64_t(k + u) * 2 * pitch] : 0.f;
+            #pragma unroll
+            for (int u = 0; u < kU; ++u) acc += v[u];
+        }
     }
     s[warp][lane] = acc;
     __syncthreads();
@@ -914,13 +935,20 @@ static RingShape ring_shape(int32_t d, int warps, int* pieces) {
 }
 
 template <typename Args>
-static dlm_status_t launch_ring(void (*kern)(Args, RingShape), const Args& a, RingShape sh, int slots, size_t more,
-                                unsigned grid, cudaStream_t s, const char* what) {
+static dlm_status_t launch_ring(void (*kern)(Args, RingShape), const Args& a, RingShape sh, int slots, unsigned grid,
+                                cudaStream_t s, const char* what) {
     const unsigned threads = unsigned(sh.nw * sh.groups * 32);
-    const size_t smem = size_t(slots) * threads * 16 + more;
+    const size_t smem = size_t(slots) * threads * 16;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) { cudaGetLastError(); return cuda_status(e, what); }
     return launch_pdl(kern, dim3(grid), dim3(threads), smem, s, what, a, sh);
+}
+
+template <int kN>
+static dlm_status_t launch_bwd_ring(const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
+    auto kern = a.format == DLM_PACK_NONE ? k_norm_bwd_ring<kN, DLM_PACK_NONE>
+              : a.format == DLM_PACK_INT8 ? k_norm_bwd_ring<kN, DLM_PACK_INT8> : k_norm_bwd_ring<kN, DLM_PACK_E4M3>;
+    return launch_ring(kern, a, sh, 2 * kN * bwd_stages<kN>(), grid, s, "k_norm_bwd launch");
 }
 
 static unsigned ring_grid(int64_t rows) { return unsigned(rows < 148 ? rows : 148); }
@@ -974,14 +1002,18 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
     const bool vec = d_model % 8 == 0 && ld_x % 8 == 0 && ld_y % 8 == 0 && aligned16(x) && aligned16(y) &&
                      param_aligned(weight) && param_aligned(bias) && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
     int pieces = 0;
-    const RingShape sh = ring_shape(d_model, kFwdThreads / 32, &pieces);
-    if (vec && sh.nw && d_model <= 8192 && rows > 148) {
-        auto kern = pieces == 1 ? (pack_format ? k_norm_fwd_ring<1, true> : k_norm_fwd_ring<1, false>)
-                                : (pack_format ? k_norm_fwd_ring<2, true> : k_norm_fwd_ring<2, false>);
-        return launch_ring(kern, a, sh, 2 * pieces * kFwdStages, 0, ring_grid(rows), s, "k_norm_fwd launch");
+    const RingShape sh = ring_shape(d_model, kRingThreads / 32, &pieces);
+    if (vec) {
+        const int nv = d_model / 8;
+        const int64_t all = rows * nv;                   // 16-byte pieces of the call
+        if (sh.nw && all >= kRingPieces && pack_format == DLM_PACK_NONE)
+            return launch_ring(pieces == 1 ? k_norm_fwd_ring<1> : k_norm_fwd_ring<2>, a, sh, 2 * pieces * kFwdStages,
+                               ring_grid(rows), s, "k_norm_fwd launch");
+        if (all <= kOnePiece && warps_for(nv, 1)) return launch_fwd_vec<1>(warps_for(nv, 1), a, s);
+        if (all <= kTwoPieces && warps_for(nv, 2)) return launch_fwd_vec<2>(warps_for(nv, 2), a, s);
+        if (warps_for(nv, 4)) return launch_fwd_vec<4>(warps_for(nv, 4), a, s);
     }
-    const int nw = vec ? warps_for(d_model / 8, 4) : warps_for(d_model, 8);
-    if (vec && nw) return launch_fwd_vec<4>(nw, a, s);
+    const int nw = warps_for(d_model, 8);
     if (nw) st = launch_fwd_any(nw, a, s);
     else st = launch_pdl(k_norm_fwd_wide, dim3(unsigned(rows < 148 * 4 ? rows : 148 * 4)), dim3(kWideThreads), 0, s,
                          "k_norm_fwd_wide launch", a);
@@ -1031,13 +1063,7 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
         if (vec && sh.nw) {
             const unsigned grid = ring_grid(rows);
             p.partials = int(grid);
-            const char* what = "k_norm_bwd launch";
-            if (pieces == 1)
-                st = launch_ring(a.x ? k_norm_bwd_ring<1, false> : k_norm_bwd_ring<1, true>, a, sh,
-                                 2 * bwd_stages<1>(), 0, grid, s, what);
-            else
-                st = launch_ring(a.x ? k_norm_bwd_ring<2, false> : k_norm_bwd_ring<2, true>, a, sh,
-                                 4 * bwd_stages<2>(), 0, grid, s, what);
+            st = pieces == 1 ? launch_bwd_ring<1>(a, sh, grid, s) : launch_bwd_ring<2>(a, sh, grid, s);
         } else if (!p.nw) st = launch_pdl(k_norm_bwd_wide, dim3(p.grid), dim3(kWideThreads), 0, s, "k_norm_bwd_wide launch", a);
         else st = launch_bwd_n(p.nw, a, p.grid, s);
         if (st != DLM_OK) return st;

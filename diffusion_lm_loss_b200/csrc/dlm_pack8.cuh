@@ -59,13 +59,11 @@ __device__ __forceinline__ void unpack_codes(uint32_t w, int format, uint64_t& l
     }
 }
 
-// max |.| of 8 bf16, as the bits of an fp32 value; those of a NaN if there is
-// one (non-negative patterns order like their values, NaN above infinity).
+// max |.| of 8 bf16 as two halves of a word (even and odd elements), by their
+// patterns: non-negative bf16 order like 16-bit integers, NaN above infinity.
 __device__ __forceinline__ uint32_t absmax8(uint4 r) {
-    auto b = [](uint32_t w) { w &= 0x7fff7fffu; return *reinterpret_cast<__nv_bfloat162*>(&w); };
-    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(b(r.x), b(r.y)), __hmax2_nan(b(r.z), b(r.w)));
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(&m) & 0x7fff7fffu;
-    return max(w << 16, w & 0xffff0000u);
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(r.x & m, r.y & m), __vmaxu2(r.z & m, r.w & m));
 }
 
 // Packs M pieces of 8 bf16, each of 16 neighbouring lanes' m-th piece making a
@@ -77,6 +75,7 @@ template <int M, typename Put>
 __device__ __forceinline__ void pack_pieces(const uint4 (&r)[M], int format, uint2 (&out)[M], Put&& put) {
     static_assert(M == 1 || M == 2 || M == 4, "pieces");
     const int lane = threadIdx.x & 31;
+    const uint64_t zero = f2negative_zero(format);
     uint32_t a[M];
     #pragma unroll
     for (int m = 0; m < M; ++m) a[m] = absmax8(r[m]);
@@ -87,23 +86,23 @@ __device__ __forceinline__ void pack_pieces(const uint4 (&r)[M], int format, uin
         #pragma unroll
         for (int k = 0; k < h; ++k) {
             const uint32_t keep = up ? a[k + h] : a[k], send = up ? a[k] : a[k + h];
-            a[k] = max(keep, __shfl_xor_sync(~0u, send, bit));
+            a[k] = __vmaxu2(keep, __shfl_xor_sync(~0u, send, bit));
         }
         mine = 2 * mine + up;
     }
     #pragma unroll
-    for (; bit; bit >>= 1) a[0] = max(a[0], __shfl_xor_sync(~0u, a[0], bit));
-    const PackFactors f = pack_factors(__uint_as_float(a[0]), format);
+    for (; bit; bit >>= 1) a[0] = __vmaxu2(a[0], __shfl_xor_sync(~0u, a[0], bit));
+    const PackFactors f = pack_factors(__uint_as_float(max(a[0] << 16, a[0] & 0xffff0000u)), format);
     if ((lane & (16 / M - 1)) == 0) put(mine, f.scale);
     #pragma unroll
     for (int m = 0; m < M; ++m) {
         const float inv = M == 1 ? f.inv : __shfl_sync(~0u, f.inv, (lane & 16) | m * (16 / M));
-        const bool none = inv == 0.f;               // zeros, or a block that is not finite
-        const uint32_t x[4] = {none ? 0u : r[m].x, none ? 0u : r[m].y, none ? 0u : r[m].z, none ? 0u : r[m].w};
+        const uint64_t inv2 = f2pack(inv, inv);
+        const uint32_t x[4] = {r[m].x, r[m].y, r[m].z, r[m].w};
         uint32_t c[4];
         #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint64_t u = f2mul_rounded(f2pack(bf16lo(x[k]), bf16hi(x[k])), inv);
+            uint64_t u = f2mul_rounded(f2pack(bf16lo(x[k]), bf16hi(x[k])), inv2, zero);
             float lo, hi;
             if (format == DLM_PACK_INT8) {
                 // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits
@@ -115,7 +114,8 @@ __device__ __forceinline__ void pack_pieces(const uint4 (&r)[M], int format, uin
                 c[k] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
             }
         }
-        out[m] = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+        const bool none = inv == 0.f;               // zeros, or a block that is not finite
+        out[m] = make_uint2(none ? 0u : __byte_perm(c[0], c[1], 0x5410), none ? 0u : __byte_perm(c[2], c[3], 0x5410));
     }
 }
 

@@ -640,7 +640,7 @@ DLM_API dlm_status_t dlm_norm_fwd(const uint16_t *x, int64_t rows, int32_t d_mod
  * reproducible.
  * x: bf16 with pack_format DLM_PACK_NONE; otherwise x is not read and
  * q, q_scale (dlm_norm_fwd's, or dlm_pack8's of x) stand for it, each element
- * code * scale in fp32.  mean and rstd are dlm_norm_fwd's (mean may be NULL
+ * code * scale (not rounded).  mean and rstd are dlm_norm_fwd's (mean may be NULL
  * for RMS).
  * workspace: at least dlm_norm_bwd_workspace_size() bytes, 256-byte aligned.
  * It has no status word: nothing here depends on device data.

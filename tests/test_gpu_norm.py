@@ -108,9 +108,9 @@ def test_checkpoint_in_8_bits(r, d, kind, fmt):
     apart = dlm.pack8(x, fmt)
     assert torch.equal(out.packed.q, apart.q) and torch.equal(out.packed.scale, apart.scale)
     q, s = ref.pack(x, fmt)
-    held = ref.held(q, s, fmt).cuda()
+    held = ref.held(q, s, fmt, torch.float64).cuda()
     got = dlm.norm_bwd(dy, out.packed, out.rstd, out.mean, w, kind, want_d_bias=True)
-    # x is the held value, an fp32 number by definition
+    # x is the held value code * scale, unrounded by definition
     _check_bwd(got, dy, held, out.mean, out.rstd, w, kind == RMS, 0.0, f32)
 
 
@@ -129,7 +129,7 @@ def test_strides_and_alignment(ld, shift, fmt):
     if fmt:
         assert torch.equal(out.packed.q, want.packed.q) and torch.equal(out.packed.scale, want.packed.scale)
     got = dlm.norm_bwd(dys, out.packed if fmt else xs, out.rstd, out.mean, w, want_d_bias=True, d_x=dx, grad_dtype=f32)
-    held = ref.held(*ref.pack(x, fmt), fmt).cuda() if fmt else x
+    held = ref.held(*ref.pack(x, fmt), fmt, torch.float64).cuda() if fmt else x
     _check_bwd(got, dy, held, out.mean, out.rstd, w, False, 0.0, f32)
     for v in (y, dx):
         v.fill_(7.0)

@@ -48,7 +48,7 @@ def test_one_step_with_a_tied_table(keep8):
     head = dlm.linear_loss_fwd_bwd(lay, n.y, table, clean, corrupted, p)
     kept = n.packed if keep8 else x
     nb = dlm.norm_bwd(head.d_hidden, kept, n.rstd, n.mean, w, want_d_bias=True)
-    held = ref.held(n.packed.q, n.packed.scale, keep8) if keep8 else x
+    held = ref.held(n.packed.q, n.packed.scale, keep8, torch.float64) if keep8 else x
     dx, dw, db = ref.norm_grad(head.d_hidden, held, n.mean, n.rstd, w, False, 0.0)
     bx, bw, bb = ref.norm_grad_bounds(head.d_hidden, held, n.mean, n.rstd, w, False, 0.0, bf16)
     ref.assert_within(nb.d_x, dx, bx, "d_x")

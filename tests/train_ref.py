@@ -128,11 +128,12 @@ def pack(x, fmt):
     return u.to(torch.float8_e4m3fn).view(torch.uint8), scale
 
 
-def held(q, scale, fmt):
-    """The fp32 values of codes and factors: code * scale, one rounding."""
-    v = (q.view(torch.int8) if fmt == INT8 else q.view(torch.float8_e4m3fn)).float()
+def held(q, scale, fmt, dtype=torch.float32):
+    """The values of codes and factors: code * scale, rounded to fp32
+    (unpack8), or in 64 bits, where it is exact (norm_bwd)."""
+    v = (q.view(torch.int8) if fmt == INT8 else q.view(torch.float8_e4m3fn)).float().to(dtype)
     d = q.shape[1]
-    return v * scale.repeat_interleave(BLOCK, 1)[:, :d]
+    return v * scale.to(dtype).repeat_interleave(BLOCK, 1)[:, :d]
 
 
 def assert_within(got, want, bound, what=""):
