@@ -4,8 +4,7 @@
 // Both are one pass over memory: 2 bytes read and 1 written per element, or
 // the reverse, and 4 bytes per 128 elements for the block's factor.  Rows
 // that start on 16-byte borders go by slabs of 1,024 columns, a warp and four
-// (packing) or eight (unpacking) loads a lane at a time; others one element a
-// lane and load, a warp per block.
+// loads a lane at a time; others by element.
 #include "dlm_host.h"
 #include "dlm_pack8.cuh"
 
@@ -43,33 +42,41 @@ __global__ void __launch_bounds__(kActThreads) k_pack8(const uint16_t* __restric
     }
 }
 
+// By element: a warp takes kAnyBlocks blocks of a row at a time, a lane the
+// elements lane, lane + 32, ... of each.
+constexpr int kAnyBlocks = 4;
+constexpr int kAnyE = kAnyBlocks * DLM_PACK_BLOCK / 32;
+
 __global__ void __launch_bounds__(kActThreads) k_pack8_any(const uint16_t* __restrict__ x, int64_t rows, int cols,
                                                            int64_t ld, int format, uint8_t* __restrict__ q,
                                                            float* __restrict__ scale) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int nb = (cols + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
-    const int64_t blocks = rows * nb;
-    const int64_t step = int64_t(gridDim.x) * (kActThreads / 32);
-    for (int64_t b = int64_t(blockIdx.x) * (kActThreads / 32) + threadIdx.x / 32; b < blocks; b += step) {
-        const int64_t r = b / nb;
-        const int c0 = int(b - r * nb) * DLM_PACK_BLOCK + lane;
-        uint16_t v[4];
-        uint32_t m = 0;
+    const int nb = (cols + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK, slabs = (nb + kAnyBlocks - 1) / kAnyBlocks;
+    const int64_t items = rows * slabs, step = int64_t(gridDim.x) * (kActThreads / 32);
+    for (int64_t i = int64_t(blockIdx.x) * (kActThreads / 32) + threadIdx.x / 32; i < items; i += step) {
+        const int64_t r = i / slabs;
+        const int b0 = int(i - r * slabs) * kAnyBlocks, c0 = b0 * DLM_PACK_BLOCK + lane;
+        const uint16_t* src = x + r * ld;
+        uint16_t v[kAnyE];
         #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = c0 + 32 * k < cols ? __ldg(x + r * ld + c0 + 32 * k) : uint16_t(0);
-            m = max(m, uint32_t(v[k] & 0x7fffu));
+        for (int k = 0; k < kAnyE; ++k) v[k] = c0 + 32 * k < cols ? __ldg(src + c0 + 32 * k) : uint16_t(0);
+        #pragma unroll
+        for (int b = 0; b < kAnyBlocks; ++b) {
+            if (b0 + b >= nb) break;
+            uint32_t m = 0;
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) m = max(m, uint32_t(v[4 * b + k] & 0x7fffu));
+            m = __reduce_max_sync(~0u, m);
+            const PackFactors f = pack_factors(__uint_as_float(m << 16), format);
+            #pragma unroll
+            for (int k = 4 * b; k < 4 * b + 4; ++k)
+                if (c0 + 32 * k < cols)
+                    q[r * cols + c0 + 32 * k] =
+                        uint8_t(pack_code(f.inv != 0.f ? bf16_bits_to_float(v[k]) : 0.f, f.inv, format));
+            if (lane == 0) scale[r * nb + b0 + b] = f.scale;
         }
-        m = __reduce_max_sync(~0u, m);
-        const PackFactors f = pack_factors(__uint_as_float(m << 16), format);
-        #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (c0 + 32 * k < cols)
-                q[r * cols + c0 + 32 * k] =
-                    uint8_t(pack_code(f.inv != 0.f ? bf16_bits_to_float(v[k]) : 0.f, f.inv, format));
-        if (lane == 0) scale[b] = f.scale;
     }
 }
 
@@ -118,27 +125,31 @@ __global__ void __launch_bounds__(kActThreads) k_unpack8_any(const uint8_t* __re
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int nb = (cols + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
-    const int64_t blocks = rows * nb, step = int64_t(gridDim.x) * (kActThreads / 32);
-    for (int64_t b = int64_t(blockIdx.x) * (kActThreads / 32) + threadIdx.x / 32; b < blocks; b += step) {
-        const int64_t r = b / nb;
-        const int c0 = int(b - r * nb) * DLM_PACK_BLOCK + lane;
-        const float s = __ldg(scale + b);
-        uint8_t v[4];
+    const int nb = (cols + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK, slabs = (nb + kAnyBlocks - 1) / kAnyBlocks;
+    const int64_t items = rows * slabs, step = int64_t(gridDim.x) * (kActThreads / 32);
+    for (int64_t i = int64_t(blockIdx.x) * (kActThreads / 32) + threadIdx.x / 32; i < items; i += step) {
+        const int64_t r = i / slabs;
+        const int b0 = int(i - r * slabs) * kAnyBlocks, c0 = b0 * DLM_PACK_BLOCK + lane;
+        const uint8_t* src = q + r * cols;
+        uint8_t v[kAnyE];
+        float s[kAnyBlocks];
         #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = c0 + 32 * k < cols ? __ldg(q + r * cols + c0 + 32 * k) : uint8_t(0);
+        for (int k = 0; k < kAnyE; ++k) v[k] = c0 + 32 * k < cols ? __ldg(src + c0 + 32 * k) : uint8_t(0);
         #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int b = 0; b < kAnyBlocks; ++b) s[b] = b0 + b < nb ? __ldg(scale + r * nb + b0 + b) : 0.f;
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k)
             if (c0 + 32 * k < cols)
-                out[r * ld + c0 + 32 * k] = __bfloat16_as_ushort(__float2bfloat16_rn(unpack_code(v[k], format) * s));
+                out[r * ld + c0 + 32 * k] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(unpack_code(v[k], format) * s[k / 4]));
     }
 }
 
 static bool pack_format_ok(int format) { return format == DLM_PACK_INT8 || format == DLM_PACK_E4M3; }
 
-// CTAs for a warp per slab (or per block of 128 columns)
+// CTAs for a warp per slab
 static unsigned act_blocks(int64_t rows, int cols, bool vec) {
-    const int width = vec ? kSlab : DLM_PACK_BLOCK, warps = kActThreads / 32;
+    const int width = vec ? kSlab : kAnyBlocks * DLM_PACK_BLOCK, warps = kActThreads / 32;
     const int64_t b = (rows * ((cols + width - 1) / width) + warps - 1) / warps;
     return unsigned(b < (1 << 20) ? b : 1 << 20);
 }

@@ -16,9 +16,10 @@
 // Backward: the columns' dw and db stay in fp32 registers over all rows of a
 // group; a CTA leaves one partial row, and k_norm_join adds the partial rows
 // in a fixed order.  x comes as bf16 or from its 8-bit checkpoint.
-// Few rows, rows too wide for a group, rows that are not on 16-byte borders:
-// kernels of one row per group of warps (k_norm_fwd), of single elements
-// (k_norm_bwd), or of any width (k_norm_*_wide).
+// Few rows, or a checkpoint to write: one row per group of warps
+// (k_norm_fwd_vec).  Rows that are not on 16-byte borders: the same rings, filled
+// by aligned chunks and read by element (k_norm_*_any).  Rows too wide for a
+// group: k_norm_*_wide.
 #include "dlm_host.h"
 #include "dlm_pack8.cuh"
 
@@ -201,53 +202,6 @@ __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd_vec
                 o[k] = f2to_bf16(f2fma(xh, f2pack(w[2 * k] + offset, w[2 * k + 1] + offset), f2pack(b[2 * k], b[2 * k + 1])));
             }
             *reinterpret_cast<uint4*>(y + c) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-    }
-}
-
-// The same by single elements: kN of them a lane, 32 * kNW apart.
-template <int kN, int kNW>
-__global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd(NormFwdArgs a) {
-    constexpr int kG = groups_per_cta(kNW);
-    __shared__ float s_x[2][kG][kNW];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = warp / kNW, wg = warp % kNW;
-    const int t = wg * 32 + lane;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t want = int64_t(blockIdx.x) * kG + g;
-    const bool live = want < a.rows;
-    const int64_t row = live ? want : a.rows - 1;
-    const uint16_t* x = a.x + row * a.ld_x;
-    float f[kN], sum = 0.f;
-    #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-        const int c = j * kNW * 32 + t;
-        f[j] = c < a.d ? bf16_bits_to_float(__ldg(x + c)) : 0.f;
-    }
-    #pragma unroll
-    for (int j = 0; j < kN; ++j) sum += f[j];
-    const float inv_d = 1.0f / float(a.d);
-    const float mean = a.rms ? 0.f : group_sum<kNW>(sum, s_x[0][g], wg) * inv_d;
-    float sq = 0.f;
-    #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-        f[j] = j * kNW * 32 + t < a.d ? f[j] - mean : 0.f;
-        sq += f[j] * f[j];
-    }
-    const float rstd = rsqrtf(group_sum<kNW>(sq, s_x[1][g], wg) * inv_d + a.eps);
-    if (!live) return;
-    if (t == 0) {
-        if (!a.rms) a.mean[row] = mean;
-        a.rstd[row] = rstd;
-    }
-    #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-        const int c = j * kNW * 32 + t;
-        if (c < a.d) {
-            const float w = a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f;
-            const float b = a.b ? param_at(a.b, a.param_f32, c) : 0.f;
-            a.y[row * a.ld_y + c] = __bfloat16_as_ushort(__float2bfloat16_rn(f[j] * rstd * w + b));
         }
     }
 }
@@ -624,6 +578,207 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     }
 }
 
+// ---------------------------------------------------------------------------
+// rows that are not on 16-byte borders
+// ---------------------------------------------------------------------------
+// A row is copied to shared memory by the aligned 16-byte chunks that cover it
+// (what a chunk holds besides the row is the tensor's own memory; the chunks
+// that would leave the tensor, at its first row's start and its last row's
+// end, are copied by element), and every thread then reads the elements
+// k * gt + t of it.  Two-byte loads from global memory would keep too few bytes
+// in flight: 13 % of the bandwidth at 8,192 rows of 5,001.
+constexpr int kAnyE = 16;             // elements a lane
+constexpr int kAnyStages = 6;
+
+// Starts the copy of `bytes` bytes at src to dst (16-byte aligned; the row
+// begins at dst + (src mod 16)); [begin, end): the tensor.
+template <typename E>
+__device__ __forceinline__ void stage_row(uint8_t* dst, const E* src, int n, const E* begin, const E* end, int t,
+                                          int gt) {
+    const uintptr_t s = reinterpret_cast<uintptr_t>(src), lo = s & ~uintptr_t(15);
+    const int chunks = int((s + size_t(n) * sizeof(E) - lo + 15) / 16);
+    for (int k = t; k < chunks; k += gt) {
+        const uintptr_t at = lo + 16u * unsigned(k);
+        if (at >= reinterpret_cast<uintptr_t>(begin) && at + 16 <= reinterpret_cast<uintptr_t>(end)) {
+            cp_async16(smem_addr(dst + 16 * k), reinterpret_cast<const void*>(at));
+        } else {
+            #pragma unroll 1
+            for (int e = 0; e < int(16 / sizeof(E)); ++e) {
+                const E* p = reinterpret_cast<const E*>(at) + e;
+                if (p >= src && p < src + n) reinterpret_cast<E*>(dst + 16 * k)[e] = *p;
+            }
+        }
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ const E* staged(const uint8_t* dst, const E* src) {
+    return reinterpret_cast<const E*>(dst + (reinterpret_cast<uintptr_t>(src) & 15));
+}
+
+__device__ __forceinline__ void group_barrier(const RingShape sh, int bar) {
+    if (sh.nw > 1) named_barrier_sync(bar, sh.nw * 32);
+    else __syncwarp();
+}
+
+__global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_any(NormFwdArgs a, RingShape sh, int slot) {
+    extern __shared__ uint4 ring_mem[];                   // [group][kAnyStages][slot bytes]
+    __shared__ float s_x[2][2][kRingThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = warp / sh.nw, wg = warp - g * sh.nw;
+    const int t = wg * 32 + lane, gt = sh.nw * 32;
+    uint8_t* ring = reinterpret_cast<uint8_t*>(ring_mem) + size_t(g) * kAnyStages * slot;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
+    const uint16_t* end = a.x + (a.rows - 1) * a.ld_x + a.d;
+    int put = 0, get = 0, par = 0;
+    auto issue = [&](int64_t row) {
+        if (row < a.rows) stage_row(ring + put * slot, a.x + row * a.ld_x, a.d, a.x, end, t, gt);
+        cp_async_commit();
+        put = put + 1 == kAnyStages ? 0 : put + 1;
+    };
+    #pragma unroll 1
+    for (int s = 0; s < kAnyStages - 1; ++s) issue(first + s * step);
+    float w[kAnyE], b[kAnyE];
+    #pragma unroll
+    for (int k = 0; k < kAnyE; ++k) {
+        const int c = k * gt + t;
+        w[k] = a.w && c < a.d ? param_at(a.w, a.param_f32, c) + a.offset : 1.f;
+        b[k] = a.b && c < a.d ? param_at(a.b, a.param_f32, c) : 0.f;
+    }
+    const float inv_d = 1.0f / float(a.d);
+    for (int64_t row = first; row < a.rows; row += step, par ^= 1) {
+        cp_async_wait<kAnyStages - 2>();
+        group_barrier(sh, 1 + g);                         // the other threads' chunks, too
+        const uint16_t* x = staged(ring + get * slot, a.x + row * a.ld_x);
+        get = get + 1 == kAnyStages ? 0 : get + 1;
+        float f[kAnyE], sum = 0.f, sq = 0.f, mean = 0.f;
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k) f[k] = k * gt + t < a.d ? bf16_bits_to_float(x[k * gt + t]) : 0.f;
+        issue(row + (kAnyStages - 1) * step);             // into the slot of the row before: all have read it
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k) sum += f[k];
+        if (!a.rms) mean = group_sum1(sum, &s_x[par][0][g * sh.nw], wg, sh, 1 + g) * inv_d;
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k) {
+            f[k] = k * gt + t < a.d ? f[k] - mean : 0.f;
+            sq += f[k] * f[k];
+        }
+        const float rstd = rsqrtf(group_sum1(sq, &s_x[par][1][g * sh.nw], wg, sh, 1 + g) * inv_d + a.eps);
+        if (t == 0) {
+            if (!a.rms) a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        uint16_t* y = a.y + row * a.ld_y;
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k)
+            if (k * gt + t < a.d)
+                y[k * gt + t] = __bfloat16_as_ushort(__float2bfloat16_rn(f[k] * rstd * w[k] + b[k]));
+    }
+    cp_async_wait<0>();
+}
+
+template <int kFormat>
+__global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_any(NormBwdArgs a, RingShape sh, int slot) {
+    constexpr bool kHeld8 = kFormat != DLM_PACK_NONE;
+    extern __shared__ uint4 ring_mem[];                   // [group][kAnyStages][dy, x: slot bytes each]; then [2][d] floats
+    __shared__ float2 s_x[2][kRingThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = warp / sh.nw, wg = warp - g * sh.nw;
+    const int t = wg * 32 + lane, gt = sh.nw * 32;
+    uint8_t* ring = reinterpret_cast<uint8_t*>(ring_mem) + size_t(g) * kAnyStages * 2 * slot;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
+    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+    const uint16_t* end_dy = a.dy + (a.rows - 1) * a.ld_dy + a.d;
+    const uint16_t* end_x = kHeld8 ? nullptr : a.x + (a.rows - 1) * a.ld_x + a.d;
+    const uint8_t* end_q = kHeld8 ? a.q + a.rows * a.d : nullptr;
+    int put = 0, get = 0, par = 0;
+    auto issue = [&](int64_t row) {
+        if (row < a.rows) {
+            uint8_t* at = ring + put * 2 * slot;
+            stage_row(at, a.dy + row * a.ld_dy, a.d, a.dy, end_dy, t, gt);
+            if constexpr (kHeld8) stage_row(at + slot, a.q + row * a.d, a.d, a.q, end_q, t, gt);
+            else stage_row(at + slot, a.x + row * a.ld_x, a.d, a.x, end_x, t, gt);
+        }
+        cp_async_commit();
+        put = put + 1 == kAnyStages ? 0 : put + 1;
+    };
+    #pragma unroll 1
+    for (int s = 0; s < kAnyStages - 1; ++s) issue(first + s * step);
+    float w[kAnyE], dw[kAnyE], db[kAnyE];
+    #pragma unroll
+    for (int k = 0; k < kAnyE; ++k) {
+        const int c = k * gt + t;
+        w[k] = a.w && c < a.d ? param_at(a.w, a.param_f32, c) + a.offset : 1.f;
+        dw[k] = db[k] = 0.f;
+    }
+    const float inv_d = 1.0f / float(a.d);
+    for (int64_t row = first; row < a.rows; row += step, par ^= 1) {
+        const float mean = a.rms ? 0.f : __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
+        cp_async_wait<kAnyStages - 2>();
+        group_barrier(sh, 1 + g);
+        const uint8_t* at = ring + get * 2 * slot;
+        const uint16_t* y = staged(at, a.dy + row * a.ld_dy);
+        get = get + 1 == kAnyStages ? 0 : get + 1;
+        float xh[kAnyE], dy[kAnyE], s1 = 0.f, s2 = 0.f;
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k) {
+            const int c = k * gt + t;
+            xh[k] = dy[k] = 0.f;
+            if (c < a.d) {
+                dy[k] = bf16_bits_to_float(y[c]);
+                float x;
+                if constexpr (kHeld8)
+                    x = fmaf(unpack_code(staged(at + slot, a.q + row * a.d)[c], kFormat),
+                             __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK), -mean);
+                else
+                    x = bf16_bits_to_float(staged(at + slot, a.x + row * a.ld_x)[c]) - mean;
+                xh[k] = x * rstd;
+            }
+        }
+        issue(row + (kAnyStages - 1) * step);
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k) {
+            const float gk = dy[k] * w[k];
+            s1 += gk;
+            s2 += gk * xh[k];
+            dw[k] += dy[k] * xh[k];
+            db[k] += dy[k];
+        }
+        group_sum2(s1, s2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
+        const float m1 = a.rms ? 0.f : s1 * inv_d, m2 = s2 * inv_d;
+        uint16_t* dx = a.dx + row * a.ld_dx;
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k)
+            if (k * gt + t < a.d)
+                dx[k * gt + t] = __bfloat16_as_ushort(__float2bfloat16_rn((dy[k] * w[k] - m1 - xh[k] * m2) * rstd));
+    }
+    // the groups' sums, added in the order of the groups
+    cp_async_wait<0>();
+    float* acc = reinterpret_cast<float*>(ring_mem);
+    for (int i = 0; i < sh.groups; ++i) {
+        __syncthreads();
+        if (g != i) continue;
+        #pragma unroll
+        for (int k = 0; k < kAnyE; ++k) {
+            const int c = k * gt + t;
+            if (c < a.d) {
+                acc[c] = i ? acc[c] + dw[k] : dw[k];
+                acc[a.d + c] = i ? acc[a.d + c] + db[k] : db[k];
+            }
+        }
+    }
+    __syncthreads();
+    float* part = a.part + int64_t(blockIdx.x) * 2 * a.pitch;
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+        if (a.want_dw) part[c] = acc[c];
+        if (a.want_db) part[a.pitch + c] = acc[a.d + c];
+    }
+}
+
 // Any width and alignment: a CTA per row, which it reads up to three times
 // (from L2 after the first).
 constexpr int kWideThreads = 512;
@@ -665,119 +820,6 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(NormFwdArgs a) {
             const float b = a.b ? param_at(a.b, a.param_f32, c) : 0.f;
             a.y[row * a.ld_y + c] = __bfloat16_as_ushort(
                 __float2bfloat16_rn((bf16_bits_to_float(__ldg(x + c)) - mean) * rstd * w + b));
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// backward by single elements
-// ---------------------------------------------------------------------------
-constexpr int kBwdN = 8;              // elements a lane, 32 * kNW apart
-
-// x - mean (x: or its checkpoint's value) and dy of this thread's columns k * 32 * kNW + t, fp32
-template <int kNW>
-__device__ __forceinline__ void bwd_load(const NormBwdArgs& a, int64_t row, int t, float mean, float (&x)[kBwdN],
-                                         float (&dy)[kBwdN]) {
-    #pragma unroll
-    for (int k = 0; k < kBwdN; ++k) {
-        const int c = k * kNW * 32 + t;
-        x[k] = dy[k] = 0.f;
-        if (c < a.d) {
-            dy[k] = bf16_bits_to_float(__ldg(a.dy + row * a.ld_dy + c));
-            if (a.x) {
-                x[k] = bf16_bits_to_float(__ldg(a.x + row * a.ld_x + c)) - mean;
-            } else {
-                const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
-                x[k] = fmaf(unpack_code(__ldg(a.q + row * a.d + c), a.format),
-                            __ldg(a.q_scale + row * nb + c / DLM_PACK_BLOCK), -mean);
-            }
-        }
-    }
-}
-
-template <int kNW>
-__global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_bwd(NormBwdArgs a) {
-    constexpr int kG = groups_per_cta(kNW);
-    constexpr int kR = 2;              // rows at a time: their loads overlap, their sums share a barrier
-    __shared__ float s_x[2][kG][kNW][2 * kR];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = warp / kNW, wg = warp % kNW;
-    const int t = wg * 32 + lane;
-    float w[kBwdN], dw[kBwdN], db[kBwdN];
-    pdl_wait();
-    pdl_launch_dependents();
-    #pragma unroll
-    for (int k = 0; k < kBwdN; ++k) {
-        const int c = (k * kNW * 32 + t);
-        w[k] = c < a.d ? (a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f) : 0.f;
-        dw[k] = db[k] = 0.f;
-    }
-    const float inv_d = 1.0f / float(a.d);
-    const int64_t groups = int64_t(gridDim.x) * kG;
-    // every group of a CTA makes the same number of turns (barriers)
-    const int64_t turns = (a.rows + groups * kR - 1) / (groups * kR);
-    int buf = 0;
-    for (int64_t i = 0; i < turns; ++i, buf ^= 1) {
-        const int64_t r0 = (i * groups + int64_t(blockIdx.x) * kG + g) * kR;
-        float x[kR][kBwdN], dy[kR][kBwdN], rstd[kR], s1[kR], s2[kR];
-        #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            const bool live = r0 + r < a.rows;
-            const int64_t row = live ? r0 + r : a.rows - 1;
-            const float mean = a.rms ? 0.f : __ldg(a.mean + row);
-            bwd_load<kNW>(a, row, t, mean, x[r], dy[r]);
-            rstd[r] = __ldg(a.rstd + row);
-            s1[r] = s2[r] = 0.f;
-            #pragma unroll
-            for (int k = 0; k < kBwdN; ++k) {
-                const float xh = x[r][k] * rstd[r];
-                x[r][k] = xh;
-                const float gk = dy[r][k] * w[k];
-                s1[r] += gk;
-                s2[r] += (k * kNW * 32 + t) < a.d ? gk * xh : 0.f;
-                if (live && (k * kNW * 32 + t) < a.d) {
-                    dw[k] += dy[r][k] * xh;
-                    db[k] += dy[r][k];
-                }
-            }
-            s1[r] = warp_sum(s1[r]);
-            s2[r] = warp_sum(s2[r]);
-        }
-        if constexpr (kNW > 1) {
-            if (lane == 0) {
-                #pragma unroll
-                for (int r = 0; r < kR; ++r) { s_x[buf][g][wg][2 * r] = s1[r]; s_x[buf][g][wg][2 * r + 1] = s2[r]; }
-            }
-            __syncthreads();
-            #pragma unroll
-            for (int r = 0; r < kR; ++r) s1[r] = s2[r] = 0.f;
-            #pragma unroll
-            for (int v = 0; v < kNW; ++v) {
-                #pragma unroll
-                for (int r = 0; r < kR; ++r) { s1[r] += s_x[buf][g][v][2 * r]; s2[r] += s_x[buf][g][v][2 * r + 1]; }
-            }
-        }
-        #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            if (r0 + r >= a.rows) break;
-            const float m1 = a.rms ? 0.f : s1[r] * inv_d, m2 = s2[r] * inv_d;
-            uint16_t* dx = a.dx + (r0 + r) * a.ld_dx;
-            float o[kBwdN];
-            #pragma unroll
-            for (int k = 0; k < kBwdN; ++k) o[k] = (dy[r][k] * w[k] - m1 - x[r][k] * m2) * rstd[r];
-            #pragma unroll
-            for (int k = 0; k < kBwdN; ++k)
-                if ((k * kNW * 32 + t) < a.d)
-                    dx[k * kNW * 32 + t] = __bfloat16_as_ushort(__float2bfloat16_rn(o[k]));
-        }
-    }
-    float* part = a.part + (int64_t(blockIdx.x) * kG + g) * 2 * a.pitch;
-    #pragma unroll
-    for (int k = 0; k < kBwdN; ++k) {
-        const int c = (k * kNW * 32 + t);
-        if (c < a.d) {
-            if (a.want_dw) part[c] = dw[k];
-            if (a.want_db) part[a.pitch + c] = db[k];
         }
     }
 }
@@ -896,33 +938,6 @@ static dlm_status_t launch_fwd_vec(int nw, const NormFwdArgs& a, cudaStream_t s)
     }
 }
 
-static dlm_status_t launch_fwd_any(int nw, const NormFwdArgs& a, cudaStream_t s) {
-    switch (nw) {
-        case 1: return launch_fwd<1>(k_norm_fwd<8, 1>, a, s);
-        case 2: return launch_fwd<2>(k_norm_fwd<8, 2>, a, s);
-        case 4: return launch_fwd<4>(k_norm_fwd<8, 4>, a, s);
-        case 8: return launch_fwd<8>(k_norm_fwd<8, 8>, a, s);
-        case 16: return launch_fwd<16>(k_norm_fwd<8, 16>, a, s);
-        default: return launch_fwd<32>(k_norm_fwd<8, 32>, a, s);
-    }
-}
-
-template <int kNW>
-static dlm_status_t launch_bwd(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
-    return launch_pdl(k_norm_bwd<kNW>, dim3(grid), dim3(kNW * groups_per_cta(kNW) * 32), 0, s, "k_norm_bwd launch", a);
-}
-
-static dlm_status_t launch_bwd_n(int nw, const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
-    switch (nw) {
-        case 1: return launch_bwd<1>(a, grid, s);
-        case 2: return launch_bwd<2>(a, grid, s);
-        case 4: return launch_bwd<4>(a, grid, s);
-        case 8: return launch_bwd<8>(a, grid, s);
-        case 16: return launch_bwd<16>(a, grid, s);
-        default: return launch_bwd<32>(a, grid, s);
-    }
-}
-
 // Ring kernels: one piece a lane up to 256 columns, two beyond, as long as 16
 // warps hold a row; nw = 0: they do not.
 static RingShape ring_shape(int32_t d, int warps, int* pieces) {
@@ -953,23 +968,36 @@ static dlm_status_t launch_bwd_ring(const NormBwdArgs& a, RingShape sh, unsigned
 
 static unsigned ring_grid(int64_t rows) { return unsigned(rows < 148 ? rows : 148); }
 
-// How the backward pass splits its rows: `grid` CTAs of the kernels by element
-// (nw warps a row; 0: the wide one).  The workspace holds the partial rows of
-// either these or the ring kernel's, so it does not depend on alignment.
-struct NormBwdPlan { int nw; unsigned grid; int partials; int pitch; size_t bytes; };
+// Kernels for any alignment: 16 elements a lane, as long as 16 warps hold a row.
+static RingShape any_shape(int32_t d) {
+    RingShape sh = {(d + 32 * kAnyE - 1) / (32 * kAnyE), 0};
+    if (sh.nw > 16) sh.nw = 0;
+    else sh.groups = kRingThreads / 32 / sh.nw < 15 || sh.nw == 1 ? kRingThreads / 32 / sh.nw : 15;
+    return sh;
+}
+
+// A slot holds a row's chunks; `acc`: shared memory that the kernel needs
+// besides (its ring is free by then).
+template <typename Args>
+static dlm_status_t launch_any(void (*kern)(Args, RingShape, int), const Args& a, RingShape sh, int tensors, size_t acc,
+                               cudaStream_t s, const char* what) {
+    const int slot = int(align_up(size_t(a.d) * 2 + 30, 16));
+    size_t smem = size_t(sh.groups) * kAnyStages * tensors * slot;
+    if (smem < acc) smem = acc;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) { cudaGetLastError(); return cuda_status(e, what); }
+    return launch_pdl(kern, dim3(ring_grid(a.rows)), dim3(unsigned(sh.nw * sh.groups * 32)), smem, s, what, a, sh, slot);
+}
+
+// The backward pass leaves one partial row per CTA, of which there is at most
+// one per SM, whatever the kernel.
+struct NormBwdPlan { unsigned grid; int pitch; size_t bytes; };
 
 static bool norm_bwd_plan(int64_t rows, int32_t d, NormBwdPlan* p) {
     if (rows < 0 || d < 1 || d > INT32_MAX - 1024) return false;
-    p->nw = warps_for(d, kBwdN);
-    const int groups = p->nw ? groups_per_cta(p->nw) : 1;
-    const int threads = p->nw ? p->nw * groups * 32 : kWideThreads;
-    const int64_t resident = 148 * int64_t(1024 / threads);
-    const int64_t need = (rows + groups - 1) / groups;
-    p->grid = unsigned(need < resident ? need : resident);
-    p->partials = int(p->grid) * groups;
+    p->grid = ring_grid(rows);
     p->pitch = int(align_up(size_t(d), 32));
-    const int most = p->partials > int(ring_grid(rows)) ? p->partials : int(ring_grid(rows));
-    p->bytes = align_up((size_t(most) * 2 + 1) * size_t(p->pitch) * 4, kWsAlign);
+    p->bytes = align_up((size_t(p->grid) * 2 + 1) * size_t(p->pitch) * 4, kWsAlign);
     return true;
 }
 
@@ -1013,8 +1041,8 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
         if (all <= kTwoPieces && warps_for(nv, 2)) return launch_fwd_vec<2>(warps_for(nv, 2), a, s);
         if (warps_for(nv, 4)) return launch_fwd_vec<4>(warps_for(nv, 4), a, s);
     }
-    const int nw = warps_for(d_model, 8);
-    if (nw) st = launch_fwd_any(nw, a, s);
+    const RingShape any = any_shape(d_model);
+    if (any.nw) st = launch_any(k_norm_fwd_any, a, any, 1, 0, s, "k_norm_fwd launch");
     else st = launch_pdl(k_norm_fwd_wide, dim3(unsigned(rows < 148 * 4 ? rows : 148 * 4)), dim3(kWideThreads), 0, s,
                          "k_norm_fwd_wide launch", a);
     if (st != DLM_OK || pack_format == DLM_PACK_NONE) return st;
@@ -1059,17 +1087,20 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
         const bool vec = d_model % 8 == 0 && ld_dy % 8 == 0 && ld_dx % 8 == 0 && aligned16(d_y) && aligned16(d_x) &&
                          (a.x ? ld_x % 8 == 0 && aligned16(x) : (reinterpret_cast<uintptr_t>(q) & 7) == 0);
         int pieces = 0;
-        const RingShape sh = ring_shape(d_model, kRingThreads / 32, &pieces);
+        const RingShape sh = ring_shape(d_model, kRingThreads / 32, &pieces), any = any_shape(d_model);
         if (vec && sh.nw) {
-            const unsigned grid = ring_grid(rows);
-            p.partials = int(grid);
-            st = pieces == 1 ? launch_bwd_ring<1>(a, sh, grid, s) : launch_bwd_ring<2>(a, sh, grid, s);
-        } else if (!p.nw) st = launch_pdl(k_norm_bwd_wide, dim3(p.grid), dim3(kWideThreads), 0, s, "k_norm_bwd_wide launch", a);
-        else st = launch_bwd_n(p.nw, a, p.grid, s);
+            st = pieces == 1 ? launch_bwd_ring<1>(a, sh, p.grid, s) : launch_bwd_ring<2>(a, sh, p.grid, s);
+        } else if (any.nw) {
+            auto kern = pack_format == DLM_PACK_NONE ? k_norm_bwd_any<DLM_PACK_NONE>
+                      : pack_format == DLM_PACK_INT8 ? k_norm_bwd_any<DLM_PACK_INT8> : k_norm_bwd_any<DLM_PACK_E4M3>;
+            st = launch_any(kern, a, any, 2, size_t(d_model) * 8, s, "k_norm_bwd launch");
+        } else {
+            st = launch_pdl(k_norm_bwd_wide, dim3(p.grid), dim3(kWideThreads), 0, s, "k_norm_bwd_wide launch", a);
+        }
         if (st != DLM_OK) return st;
     }
     if (!d_weight && !d_bias) return DLM_OK;
     return launch_pdl(k_norm_join, dim3(unsigned((d_model + 31) / 32), 2), dim3(kNormJoinWarps * 32), 0, s,
-                      "k_norm_join launch", (const float*)a.part, p.partials, p.pitch, d_model,
+                      "k_norm_join launch", (const float*)a.part, int(p.grid), p.pitch, d_model,
                       int(grad_dtype == DLM_F32), accumulate, d_weight, d_bias);
 }
