@@ -269,7 +269,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream of the current device, as an address (the raw
+    lookup: building torch.cuda.current_stream() costs 3 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ok(code: int, where: str):
@@ -414,8 +416,11 @@ class LinearOut:
 def _aligned_workspace(nbytes: int, device, align: int = 1024) -> torch.Tensor:
     """A uint8 workspace whose first byte is `align`-byte aligned (the loss
     needs 256, the fused head 1024; the caching allocator guarantees 512 and
-    other allocators less): a slice of a slightly larger buffer, which the
-    slice keeps alive."""
+    other allocators less): where it is not, a slice of a slightly larger
+    buffer, which the slice keeps alive."""
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if buf.data_ptr() % align == 0:
+        return buf
     buf = torch.empty(nbytes + align - 1, dtype=torch.uint8, device=device)
     off = (-buf.data_ptr()) % align
     return buf[off:off + nbytes]
@@ -615,6 +620,13 @@ def _call(dev: torch.device, name: str, *args):
 def _check_rows(t: Optional[torch.Tensor], dtype, name: str, rows: int, cols: int) -> int:
     """A [rows, cols] argument with unit column stride (`rows`: at least so
     many); its row stride."""
+    if t is not None and t.dtype is dtype and t.dim() == 2:     # the usual case, without a message to word
+        (n, m), (ld, unit) = t.shape, t.stride()
+        if n >= rows and m == cols and (unit == 1 or cols <= 1):
+            if n <= 1:
+                return cols
+            if ld >= cols:
+                return ld
     _check(t, dtype, name, min_rows=rows)
     if t.shape[1] != cols:
         raise ValueError(f"{name}: must have {cols} columns, has {t.shape[1]}")
@@ -622,6 +634,12 @@ def _check_rows(t: Optional[torch.Tensor], dtype, name: str, rows: int, cols: in
     if ld < cols:
         raise ValueError(f"{name}: rows overlap (row stride {ld}, {cols} columns)")
     return ld
+
+
+def _shape2(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: must be 2-D, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 def _as_rows(t: torch.Tensor) -> torch.Tensor:
@@ -644,7 +662,6 @@ def embed_fwd(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: fl
     DEV_BAD_TOKEN_ID or'ed in when an id is outside the table."""
     T = layout.n_tokens
     _check(ids, torch.int32, "ids", min_numel=T)
-    _check(weight, torch.bfloat16, "weight")
     if weight.dim() != 2 or weight.shape[0] < 1 or weight.shape[1] < 1:
         raise ValueError("weight: [vocab, d_model]")
     V, D = weight.shape
@@ -681,8 +698,7 @@ def embed_bwd(layout: Layout, ids: torch.Tensor, d_out: torch.Tensor, vocab: int
     what d_weight holds, e.g. the d_weight of a tied output head."""
     T = layout.n_tokens
     _check(ids, torch.int32, "ids", min_numel=T)
-    _check(d_out, torch.bfloat16, "d_out", min_rows=T)
-    D = d_out.shape[1]
+    D = d_out.shape[1] if d_out.dim() == 2 else 1
     if D < 1 or vocab < 1:
         raise ValueError("d_out and the table need at least one column and one row")
     ld = _check_rows(d_out, torch.bfloat16, "d_out", T, D)
@@ -735,8 +751,7 @@ def _check_packed(p: Packed8, rows: int, cols: int, name: str):
 def pack8(x: torch.Tensor, format: int = PACK_INT8, out: Optional[Packed8] = None) -> Packed8:
     """x (bf16 [rows, cols]) in 8 bits, one float factor per PACK_BLOCK
     columns (see dlm_pack8)."""
-    _check(x, torch.bfloat16, "x", min_rows=0)
-    rows, cols = x.shape
+    rows, cols = _shape2(x, "x")
     ld = _check_rows(x, torch.bfloat16, "x", rows, cols)
     if out is not None:
         _check_packed(out, rows, cols, "out")
@@ -779,8 +794,8 @@ def _check_params(weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], 
         if t is None:
             continue
         dt = _param_dtype(t.dtype, name)
-        _check(t, t.dtype, name, min_numel=cols)
-        if t.dim() != 1 or t.numel() != cols:
+        if t.dim() != 1 or t.numel() != cols or not t.is_contiguous():
+            _check(t, t.dtype, name, min_numel=cols)
             raise ValueError(f"{name}: must have shape ({cols},), has {tuple(t.shape)}")
         if dtype is not None and dt != dtype:
             raise TypeError("weight and bias: must have one type")
@@ -794,8 +809,7 @@ def norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optio
     """Layer norm or RMS norm of the rows of x (bf16 [rows, d_model]; see
     dlm_norm_fwd).  pack: also x in 8 bits, which norm_bwd takes in x's place.
     Reuses the buffers of `out` when given."""
-    _check(x, torch.bfloat16, "x", min_rows=0)
-    rows, D = x.shape
+    rows, D = _shape2(x, "x")
     ld = _check_rows(x, torch.bfloat16, "x", rows, D)
     pt = _check_params(weight, bias, D)
     if pack not in (PACK_NONE, PACK_INT8, PACK_E4M3):
@@ -817,10 +831,13 @@ def norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optio
     else:
         _on_cuda(x=x, weight=weight, bias=bias)
         dev = x.device
-        stats = torch.empty((2 if layer else 1, rows), dtype=torch.float32, device=dev)
+        if layer:
+            stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
+            rstd, mean = stats[0], stats[1]
+        else:
+            rstd, mean = torch.empty(rows, dtype=torch.float32, device=dev), None
         pk = _empty_packed(rows, D, pack, dev) if pack != PACK_NONE else None
-        out = NormOut(torch.empty((rows, D), dtype=torch.bfloat16, device=dev), stats[1] if layer else None, stats[0],
-                      pk)
+        out = NormOut(torch.empty((rows, D), dtype=torch.bfloat16, device=dev), mean, rstd, pk)
     _call(x.device, "dlm_norm_fwd", _ptr(x), rows, D, ld, _ptr(weight), _ptr(bias), pt, kind, eps, weight_offset,
           _ptr(out.y), ld_y, _ptr(out.mean) if layer else None, _ptr(out.rstd), pack,
           _ptr(pk.q) if pk is not None else None, _ptr(pk.scale) if pk is not None else None)
@@ -850,8 +867,7 @@ def norm_bwd(d_y: torch.Tensor, x, rstd: torch.Tensor, mean: Optional[torch.Tens
     a weight) and d_bias (with want_d_bias) come in grad_dtype (by default the
     weight's type, else float32) or in the tensors given, which accumulate
     adds to."""
-    _check(d_y, torch.bfloat16, "d_y", min_rows=0)
-    rows, D = d_y.shape
+    rows, D = _shape2(d_y, "d_y")
     ld_dy = _check_rows(d_y, torch.bfloat16, "d_y", rows, D)
     pt = _check_params(weight, None, D)
     packed = isinstance(x, Packed8)
@@ -890,6 +906,9 @@ def norm_bwd(d_y: torch.Tensor, x, rstd: torch.Tensor, mean: Optional[torch.Tens
     dev = d_y.device
     if d_x is None:
         d_x = torch.empty((rows, D), dtype=torch.bfloat16, device=dev)
+    if want_w and want_b and d_weight is None and d_bias is None:
+        both = torch.empty((2, D), dtype=grad_dtype, device=dev)
+        d_weight, d_bias = both[0], both[1]
     if want_w and d_weight is None:
         d_weight = torch.empty(D, dtype=grad_dtype, device=dev)
     if want_b and d_bias is None:
