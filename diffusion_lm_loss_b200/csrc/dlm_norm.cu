@@ -17,9 +17,10 @@
 // group; a CTA leaves one partial row, and k_norm_join adds the partial rows
 // in a fixed order.  x comes as bf16 or from its 8-bit checkpoint.
 // Few rows, or a checkpoint to write: one row per group of warps
-// (k_norm_fwd_vec).  Rows that are not on 16-byte borders: the same rings, filled
-// by aligned chunks and read by element (k_norm_*_any).  Rows too wide for a
-// group: k_norm_*_wide.
+// (k_norm_fwd_vec).  Rows that are not on 16-byte borders, but in step with one
+// another (all tensors contiguous, an odd width): the rings again, by aligned
+// chunks (kShift).  Rows out of step: rings read by element (k_norm_*_any).
+// Rows too wide for a group: k_norm_*_wide.
 #include "dlm_host.h"
 #include "dlm_pack8.cuh"
 
@@ -308,35 +309,102 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
     return v;
 }
 
-template <int kN>
+// Where a thread's pieces lie.  With kShift the rows are not on 16-byte borders:
+// a piece is an aligned 16-byte chunk of memory all the same, and holds the
+// columns 8 p - phase .. 8 p - phase + 7, phase = (row x stride) mod 8.  All rows
+// of a group have one phase (their distance is a multiple of 8), so a thread
+// keeps its columns, whose parameters and sums stay in its registers.  The
+// first piece may begin with the end of the row before (masked after the load),
+// the last one may end behind the row (not read); both are stored by element.
+template <int kN, bool kShift>
+struct Pieces {
+    int c[kN];             // first column
+    bool in[kN], edge[kN];
+    __device__ __forceinline__ Pieces(int t, int gt, int d, int phase) {
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            c[j] = (j * gt + t) * 8 - (kShift ? phase : 0);
+            in[j] = c[j] < d;
+            edge[j] = kShift && in[j] && (c[j] < 0 || c[j] + 8 > d);
+        }
+    }
+    // bytes of the piece that are read: all but those behind the row
+    template <typename E>
+    __device__ __forceinline__ int bytes(int j, int d) const {
+        return int(sizeof(E)) * min(8, d - c[j]);
+    }
+    // zero outside the row
+    __device__ __forceinline__ void clip(int j, int d, uint64_t (&f)[4]) const {
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            f2unpack(f[k], lo, hi);
+            const int e = c[j] + 2 * k;
+            f[k] = f2pack(e >= 0 && e < d ? lo : 0.f, e + 1 >= 0 && e + 1 < d ? hi : 0.f);
+        }
+    }
+    __device__ __forceinline__ void params(int j, int d, const void* p, int f32, float none, float add,
+                                           uint64_t (&o)[4]) const {
+        if (!kShift) {
+            param_pairs(p, f32, in[j] ? c[j] : 0, none, add, o);
+        } else {
+            float v[8];
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int e = c[j] + k;
+                v[k] = p && e >= 0 && e < d ? param_at(p, f32, e) + add : none;
+            }
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = f2pack(v[2 * k], v[2 * k + 1]);
+        }
+    }
+    // stores the piece at `at`, its aligned place in the row
+    __device__ __forceinline__ void store(int j, int d, uint16_t* at, const uint64_t (&v)[4]) const {
+        uint32_t o[4];
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = f2to_bf16(v[k]);
+        if (kShift && edge[j]) {
+            #pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c[j] + k >= 0 && c[j] + k < d) at[k] = uint16_t(o[k / 2] >> (16 * (k & 1)));
+        } else if (in[j]) {
+            *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+};
+
+template <int kN, bool kShift>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a, RingShape sh) {
     constexpr int kS = kFwdStages, kR = 2;                // two rows at a time: their exchanges share barriers
     extern __shared__ uint4 ring_mem[];
-    __shared__ float2 s_x[2][2][kRingThreads / 32];        // [turn parity][sum][warp]
+    __shared__ float2 s_x[2][2][kRingThreads / 32];       // [turn parity][sum][warp]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = warp / sh.nw, wg = warp - g * sh.nw;
     const int t = wg * 32 + lane, gt = sh.nw * 32;
-    bool in[kN];
-    #pragma unroll
-    for (int j = 0; j < kN; ++j) in[j] = (j * gt + t) * 8 < a.d;
+    const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
+    const int phase = kShift ? int((first * a.ld_x) & 7) : 0;
+    const Pieces<kN, kShift> pc(t, gt, a.d, phase);
     Ring<kS, kR * kN> ring(ring_mem);
     #pragma unroll
     for (int j = 0; j < kR * kN; ++j)
-        if (!in[j % kN]) ring.clear(ring_mem, j);
+        if (!pc.in[j % kN]) ring.clear(ring_mem, j);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
     int n = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
     const int64_t dx = step * a.ld_x, dy = step * a.ld_y;
-    const uint16_t* px = a.x + first * a.ld_x + t * 8;
+    const uint16_t* px = a.x + first * a.ld_x + t * 8 - phase;
     int left = n;
     auto issue = [&]() {
         #pragma unroll
         for (int r = 0; r < kR; ++r) {
             if (left > 0) {
                 #pragma unroll
-                for (int j = 0; j < kN; ++j)
-                    if (in[j]) cp_async16(ring.put + (r * kN + j) * ring.pitch, px + j * gt * 8);
+                for (int j = 0; j < kN; ++j) {
+                    const uint32_t dst = ring.put + (r * kN + j) * ring.pitch;
+                    if (!pc.in[j]) continue;
+                    if constexpr (kShift) cp_async16_part(dst, px + j * gt * 8, pc.template bytes<uint16_t>(j, a.d));
+                    else cp_async16(dst, px + j * gt * 8);
+                }
                 px += dx;
                 --left;
             }
@@ -349,12 +417,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
     uint64_t w[kN][4], b[kN][4];
     #pragma unroll
     for (int j = 0; j < kN; ++j) {
-        const int c = in[j] ? (j * gt + t) * 8 : 0;
-        param_pairs(a.w, a.param_f32, c, 1.f, a.w ? a.offset : 0.f, w[j]);
-        param_pairs(a.b, a.param_f32, c, 0.f, 0.f, b[j]);
+        pc.params(j, a.d, a.w, a.param_f32, 1.f, a.w ? a.offset : 0.f, w[j]);
+        pc.params(j, a.d, a.b, a.param_f32, 0.f, 0.f, b[j]);
     }
     const float inv_d = 1.0f / float(a.d);
-    uint16_t* py = a.y + first * a.ld_y + t * 8;
+    uint16_t* py = a.y + first * a.ld_y + t * 8 - phase;
     int par = 0;
     int64_t row = first;
     for (; n > 0; n -= kR, par ^= 1, row += kR * step, py += kR * dy) {
@@ -369,7 +436,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
                 const uint4 raw = lds16(ring.get + (r * kN + j) * ring.pitch);
                 const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) { f[r][j][k] = f2bf16(u[k]); sum = f2add(sum, f[r][j][k]); }
+                for (int k = 0; k < 4; ++k) f[r][j][k] = f2bf16(u[k]);
+                if (kShift && pc.edge[j]) pc.clip(j, a.d, f[r][j]);
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) sum = f2add(sum, f[r][j][k]);
             }
             f2unpack(sum, lo, hi);
             s1[r] = lo + hi;
@@ -384,12 +454,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
             uint64_t sq = 0;
             #pragma unroll
             for (int j = 0; j < kN; ++j) {
-                const uint64_t nm = f2splat(in[j] ? -s1[r] : 0.f);
+                const uint64_t nm = f2splat(pc.in[j] ? -s1[r] : 0.f);
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    f[r][j][k] = f2add(f[r][j][k], nm);
-                    sq = f2fma(f[r][j][k], f[r][j][k], sq);
-                }
+                for (int k = 0; k < 4; ++k) f[r][j][k] = f2add(f[r][j][k], nm);
+                if (kShift && pc.edge[j]) pc.clip(j, a.d, f[r][j]);
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) sq = f2fma(f[r][j][k], f[r][j][k], sq);
             }
             f2unpack(sq, lo, hi);
             s2[r] = lo + hi;
@@ -406,12 +476,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
             const uint64_t r2 = f2splat(rstd);
             #pragma unroll
             for (int j = 0; j < kN; ++j) {
-                if (in[j]) {
-                    uint32_t o[4];
-                    #pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = f2to_bf16(f2fma(f2mul(f[r][j][k], r2), w[j][k], b[j][k]));
-                    *reinterpret_cast<uint4*>(py + r * dy + j * gt * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
+                uint64_t o[4];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = f2fma(f2mul(f[r][j][k], r2), w[j][k], b[j][k]);
+                pc.store(j, a.d, py + r * dy + j * gt * 8, o);
             }
         }
     }
@@ -419,40 +487,46 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
 }
 
 // kFormat: DLM_PACK_NONE (x itself) or the format of its checkpoint
-template <int kN, int kFormat>
+template <int kN, int kFormat, bool kShift>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a, RingShape sh) {
     constexpr int kS = bwd_stages<kN>();
     constexpr bool kHeld8 = kFormat != DLM_PACK_NONE;
-    extern __shared__ uint4 ring_mem[];                   // ring of dy, x pieces; at the end [2][d] floats
+    extern __shared__ uint4 ring_mem[];                   // ring of dy, x pieces; at the end the groups' sums
     __shared__ float2 s_x[2][16];                         // [row parity][warp]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = warp / sh.nw, wg = warp - g * sh.nw;
     const int t = wg * 32 + lane, gt = sh.nw * 32;
     uint64_t w[kN][4], dw[kN][4], db[kN][4];
-    bool in[kN];
-    #pragma unroll
-    for (int j = 0; j < kN; ++j) in[j] = (j * gt + t) * 8 < a.d;
+    const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
+    const int phase = kShift ? int((first * a.ld_dy) & 7) : 0;
+    const Pieces<kN, kShift> pc(t, gt, a.d, phase);
     Ring<kS, 2 * kN> ring(ring_mem);
     #pragma unroll
     for (int j = 0; j < 2 * kN; ++j)
-        if (!in[j / 2]) ring.clear(ring_mem, j);
+        if (!pc.in[j / 2]) ring.clear(ring_mem, j);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
     int n = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
     const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
-    const uint16_t* pdy = a.dy + first * a.ld_dy + t * 8;
-    const uint16_t* px = kHeld8 ? nullptr : a.x + first * a.ld_x + t * 8;
-    const uint8_t* pq = kHeld8 ? a.q + first * a.d + t * 8 : nullptr;
+    const uint16_t* pdy = a.dy + first * a.ld_dy + t * 8 - phase;
+    const uint16_t* px = kHeld8 ? nullptr : a.x + first * a.ld_x + t * 8 - phase;
+    const uint8_t* pq = kHeld8 ? a.q + first * a.d + t * 8 - phase : nullptr;
     int left = n;
     auto issue = [&]() {
         if (left > 0) {
             #pragma unroll
             for (int j = 0; j < kN; ++j) {
-                if (in[j]) {
-                    cp_async16(ring.put + 2 * j * ring.pitch, pdy + j * gt * 8);
-                    if constexpr (kHeld8) cp_async8(ring.put + (2 * j + 1) * ring.pitch, pq + j * gt * 8);
-                    else cp_async16(ring.put + (2 * j + 1) * ring.pitch, px + j * gt * 8);
+                if (!pc.in[j]) continue;
+                const uint32_t dst = ring.put + 2 * j * ring.pitch;
+                if constexpr (kShift) {
+                    const int nb16 = pc.template bytes<uint16_t>(j, a.d);
+                    cp_async16_part(dst, pdy + j * gt * 8, nb16);
+                    if constexpr (kHeld8) cp_async8_part(dst + ring.pitch, pq + j * gt * 8, nb16 / 2);
+                    else cp_async16_part(dst + ring.pitch, px + j * gt * 8, nb16);
+                } else {
+                    cp_async16(dst, pdy + j * gt * 8);
+                    if constexpr (kHeld8) cp_async8(dst + ring.pitch, pq + j * gt * 8);
+                    else cp_async16(dst + ring.pitch, px + j * gt * 8);
                 }
             }
             pdy += step * a.ld_dy;
@@ -467,7 +541,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     const float* pmean = a.mean + first;
     const float* prstd = a.rstd + first;
     const float* pqs = kHeld8 ? a.q_scale + first * nb : nullptr;
-    float mean_n = 0.f, rstd_n = 0.f, qs_n[kN];
+    float mean_n = 0.f, rstd_n = 0.f, qs_n[kN], qs2_n[kN];   // qs2: of the second block in a piece that holds two
+    int two[kN];                                             // elements of the first one there, 8 if there is one only
+    #pragma unroll
+    for (int j = 0; j < kN; ++j)
+        two[j] = kShift && pc.in[j] && (pc.c[j] & 127) > 120 && (pc.c[j] | 127) + 1 < a.d ? 128 - (pc.c[j] & 127) : 8;
     auto next_stats = [&](bool more) {
         if (!more) return;
         if (!a.rms) mean_n = __ldg(pmean);
@@ -476,7 +554,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
         prstd += step;
         if constexpr (kHeld8) {
             #pragma unroll
-            for (int j = 0; j < kN; ++j) qs_n[j] = in[j] ? __ldg(pqs + (j * gt + t) * 8 / DLM_PACK_BLOCK) : 0.f;
+            for (int j = 0; j < kN; ++j) {
+                const int b0 = max(pc.c[j], 0) / DLM_PACK_BLOCK;
+                qs_n[j] = pc.in[j] ? __ldg(pqs + b0) : 0.f;
+                if (kShift) qs2_n[j] = two[j] < 8 ? __ldg(pqs + (pc.c[j] + 8) / DLM_PACK_BLOCK) : 0.f;
+            }
             pqs += step * nb;
         }
     };
@@ -485,19 +567,19 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     next_stats(n > 0);
     #pragma unroll
     for (int j = 0; j < kN; ++j) {
-        param_pairs(a.w, a.param_f32, in[j] ? (j * gt + t) * 8 : 0, 1.f, a.w ? a.offset : 0.f, w[j]);
+        pc.params(j, a.d, a.w, a.param_f32, 1.f, a.w ? a.offset : 0.f, w[j]);
         #pragma unroll
         for (int k = 0; k < 4; ++k) dw[j][k] = db[j][k] = 0;
     }
     const float inv_d = 1.0f / float(a.d);
-    uint16_t* pdx = a.dx + first * a.ld_dx + t * 8;
+    uint16_t* pdx = a.dx + first * a.ld_dx + t * 8 - phase;
     int par = 0;
     for (; n > 0; --n, par ^= 1, pdx += step * a.ld_dx) {
         const uint64_t nm = f2splat(-mean_n), r2 = f2splat(rstd_n);
-        float qs[kN];
+        float qs[kN], qs2[kN];
         if constexpr (kHeld8) {
             #pragma unroll
-            for (int j = 0; j < kN; ++j) qs[j] = qs_n[j];
+            for (int j = 0; j < kN; ++j) { qs[j] = qs_n[j]; qs2[j] = kShift ? qs2_n[j] : 0.f; }
         }
         next_stats(n > 1);
         cp_async_wait<kS - 2>();
@@ -512,16 +594,28 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
                 unpack_codes(q2.y, kFormat, xh[j][2], xh[j][3]);
                 // code * scale - mean in one FMA: the held value is not rounded
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) xh[j][k] = f2fma(xh[j][k], f2splat(qs[j]), nm);
+                for (int k = 0; k < 4; ++k) {
+                    uint64_t s = f2splat(qs[j]);
+                    if (kShift && two[j] < 8)
+                        s = f2pack(2 * k < two[j] ? qs[j] : qs2[j], 2 * k + 1 < two[j] ? qs[j] : qs2[j]);
+                    xh[j][k] = f2fma(xh[j][k], s, nm);
+                }
             } else {
                 const uint4 x4 = lds16(ring.get + (2 * j + 1) * ring.pitch);
                 const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) xh[j][k] = f2add(f2bf16(xw[k]), nm);
             }
+            uint64_t dy4[4];
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) dy4[k] = f2bf16(yw[k]);
+            if (kShift && pc.edge[j]) {                   // the end of the row before
+                pc.clip(j, a.d, xh[j]);
+                pc.clip(j, a.d, dy4);
+            }
             #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint64_t dy = f2bf16(yw[k]);
+                const uint64_t dy = dy4[k];
                 xh[j][k] = f2mul(xh[j][k], r2);
                 gr[j][k] = f2mul(dy, w[j][k]);
                 s1 = f2add(s1, gr[j][k]);
@@ -541,40 +635,38 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
         const uint64_t n1 = f2splat(a.rms ? 0.f : -v1 * inv_d), n2 = f2splat(-v2 * inv_d);
         #pragma unroll
         for (int j = 0; j < kN; ++j) {
-            if (in[j]) {
-                uint32_t o[4];
-                #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    o[k] = f2to_bf16(f2mul(f2add(f2fma(xh[j][k], n2, gr[j][k]), n1), r2));
-                *reinterpret_cast<uint4*>(pdx + j * gt * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+            uint64_t o[4];
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = f2mul(f2add(f2fma(xh[j][k], n2, gr[j][k]), n1), r2);
+            pc.store(j, a.d, pdx + j * gt * 8, o);
         }
     }
-    // the groups' sums, added in the order of the groups
+    // the groups' sums, side by side in shared memory, then added column by
+    // column in the order of the groups
     cp_async_wait<0>();
-    float* acc = reinterpret_cast<float*>(ring_mem);
-    for (int k = 0; k < sh.groups; ++k) {
-        __syncthreads();
-        if (g != k) continue;
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(ring_mem);      // [group][dw, db][kN gt 8]
+    const int wide = kN * gt * 8;
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
         #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            if (!in[j]) continue;
+        for (int h = 0; h < 2; ++h) {
+            uint64_t* p = reinterpret_cast<uint64_t*>(acc + (2 * g + h) * wide + (j * gt + t) * 8);
             #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint64_t* p = reinterpret_cast<uint64_t*>(acc + h * a.d + (j * gt + t) * 8);
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint64_t v = h ? db[j][i] : dw[j][i];
-                    p[i] = k ? f2add(p[i], v) : v;
-                }
-            }
+            for (int i = 0; i < 4; ++i) p[i] = h ? db[j][i] : dw[j][i];
         }
     }
     __syncthreads();
     float* part = a.part + int64_t(blockIdx.x) * 2 * a.pitch;
     for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-        if (a.want_dw) part[c] = acc[c];
-        if (a.want_db) part[a.pitch + c] = acc[a.d + c];
+        float sw = 0.f, sb = 0.f;
+        for (int k = 0; k < sh.groups; ++k) {
+            const int at = 2 * k * wide + c + (kShift ? int(((int64_t(k) * gridDim.x + blockIdx.x) * a.ld_dy) & 7) : 0);
+            sw += acc[at];
+            sb += acc[at + wide];
+        }
+        if (a.want_dw) part[c] = sw;
+        if (a.want_db) part[a.pitch + c] = sb;
     }
 }
 
@@ -940,8 +1032,8 @@ static dlm_status_t launch_fwd_vec(int nw, const NormFwdArgs& a, cudaStream_t s)
 
 // Ring kernels: one piece a lane up to 256 columns, two beyond, as long as 16
 // warps hold a row; nw = 0: they do not.
-static RingShape ring_shape(int32_t d, int warps, int* pieces) {
-    const int nv = (d + 7) / 8;
+static RingShape ring_shape(int32_t d, bool shift, int warps, int* pieces) {
+    const int nv = (d + 7) / 8 + (shift ? 1 : 0);        // a row may reach into one chunk more
     *pieces = nv <= 32 ? 1 : 2;
     RingShape sh = {(nv + 32 * *pieces - 1) / (32 * *pieces), 0};
     if (sh.nw > 16) sh.nw = 0;
@@ -959,14 +1051,24 @@ static dlm_status_t launch_ring(void (*kern)(Args, RingShape), const Args& a, Ri
     return launch_pdl(kern, dim3(grid), dim3(threads), smem, s, what, a, sh);
 }
 
-template <int kN>
+template <int kN, bool kShift>
 static dlm_status_t launch_bwd_ring(const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
-    auto kern = a.format == DLM_PACK_NONE ? k_norm_bwd_ring<kN, DLM_PACK_NONE>
-              : a.format == DLM_PACK_INT8 ? k_norm_bwd_ring<kN, DLM_PACK_INT8> : k_norm_bwd_ring<kN, DLM_PACK_E4M3>;
+    auto kern = a.format == DLM_PACK_NONE ? k_norm_bwd_ring<kN, DLM_PACK_NONE, kShift>
+              : a.format == DLM_PACK_INT8 ? k_norm_bwd_ring<kN, DLM_PACK_INT8, kShift>
+                                          : k_norm_bwd_ring<kN, DLM_PACK_E4M3, kShift>;
     return launch_ring(kern, a, sh, 2 * kN * bwd_stages<kN>(), grid, s, "k_norm_bwd launch");
 }
 
 static unsigned ring_grid(int64_t rows) { return unsigned(rows < 148 ? rows : 148); }
+
+// CTAs for rows that are not on 16-byte borders: the rows of a group are a
+// multiple of 8 apart.
+static unsigned shift_grid(int64_t rows, RingShape sh) {
+    unsigned grid = ring_grid(rows);
+    if (rows > grid)
+        while (grid * unsigned(sh.groups) % 8) --grid;
+    return grid;
+}
 
 // Kernels for any alignment: 16 elements a lane, as long as 16 warps hold a row.
 static RingShape any_shape(int32_t d) {
@@ -1030,19 +1132,25 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
     const bool vec = d_model % 8 == 0 && ld_x % 8 == 0 && ld_y % 8 == 0 && aligned16(x) && aligned16(y) &&
                      param_aligned(weight) && param_aligned(bias) && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
     int pieces = 0;
-    const RingShape sh = ring_shape(d_model, kRingThreads / 32, &pieces);
+    RingShape sh = ring_shape(d_model, false, kRingThreads / 32, &pieces);
     if (vec) {
         const int nv = d_model / 8;
         const int64_t all = rows * nv;                   // 16-byte pieces of the call
         if (sh.nw && all >= kRingPieces && pack_format == DLM_PACK_NONE)
-            return launch_ring(pieces == 1 ? k_norm_fwd_ring<1> : k_norm_fwd_ring<2>, a, sh, 2 * pieces * kFwdStages,
-                               ring_grid(rows), s, "k_norm_fwd launch");
+            return launch_ring(pieces == 1 ? k_norm_fwd_ring<1, false> : k_norm_fwd_ring<2, false>, a, sh,
+                               2 * pieces * kFwdStages, ring_grid(rows), s, "k_norm_fwd launch");
         if (all <= kOnePiece && warps_for(nv, 1)) return launch_fwd_vec<1>(warps_for(nv, 1), a, s);
         if (all <= kTwoPieces && warps_for(nv, 2)) return launch_fwd_vec<2>(warps_for(nv, 2), a, s);
         if (warps_for(nv, 4)) return launch_fwd_vec<4>(warps_for(nv, 4), a, s);
     }
+    // rows of x and y in step with one another, if not with the 16-byte borders
+    const bool shift = aligned16(x) && aligned16(y) && (ld_x - ld_y) % 8 == 0;
+    sh = ring_shape(d_model, true, kRingThreads / 32, &pieces);
     const RingShape any = any_shape(d_model);
-    if (any.nw) st = launch_any(k_norm_fwd_any, a, any, 1, 0, s, "k_norm_fwd launch");
+    if (shift && sh.nw)
+        st = launch_ring(pieces == 1 ? k_norm_fwd_ring<1, true> : k_norm_fwd_ring<2, true>, a, sh,
+                         2 * pieces * kFwdStages, shift_grid(rows, sh), s, "k_norm_fwd launch");
+    else if (any.nw) st = launch_any(k_norm_fwd_any, a, any, 1, 0, s, "k_norm_fwd launch");
     else st = launch_pdl(k_norm_fwd_wide, dim3(unsigned(rows < 148 * 4 ? rows : 148 * 4)), dim3(kWideThreads), 0, s,
                          "k_norm_fwd_wide launch", a);
     if (st != DLM_OK || pack_format == DLM_PACK_NONE) return st;
@@ -1086,10 +1194,17 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
     if (rows > 0) {
         const bool vec = d_model % 8 == 0 && ld_dy % 8 == 0 && ld_dx % 8 == 0 && aligned16(d_y) && aligned16(d_x) &&
                          (a.x ? ld_x % 8 == 0 && aligned16(x) : (reinterpret_cast<uintptr_t>(q) & 7) == 0);
+        // rows in step with one another, if not with the 16-byte borders
+        const bool shift = aligned16(d_y) && aligned16(d_x) && (ld_dy - ld_dx) % 8 == 0 &&
+                           (a.x ? aligned16(x) && (ld_dy - ld_x) % 8 == 0
+                                : (reinterpret_cast<uintptr_t>(q) & 7) == 0 && (ld_dy - d_model) % 8 == 0);
         int pieces = 0;
-        const RingShape sh = ring_shape(d_model, kRingThreads / 32, &pieces), any = any_shape(d_model);
+        const RingShape sh = ring_shape(d_model, !vec, kRingThreads / 32, &pieces), any = any_shape(d_model);
         if (vec && sh.nw) {
-            st = pieces == 1 ? launch_bwd_ring<1>(a, sh, p.grid, s) : launch_bwd_ring<2>(a, sh, p.grid, s);
+            st = pieces == 1 ? launch_bwd_ring<1, false>(a, sh, p.grid, s) : launch_bwd_ring<2, false>(a, sh, p.grid, s);
+        } else if (shift && sh.nw) {
+            p.grid = shift_grid(rows, sh);
+            st = pieces == 1 ? launch_bwd_ring<1, true>(a, sh, p.grid, s) : launch_bwd_ring<2, true>(a, sh, p.grid, s);
         } else if (any.nw) {
             auto kern = pack_format == DLM_PACK_NONE ? k_norm_bwd_any<DLM_PACK_NONE>
                       : pack_format == DLM_PACK_INT8 ? k_norm_bwd_any<DLM_PACK_INT8> : k_norm_bwd_any<DLM_PACK_E4M3>;
