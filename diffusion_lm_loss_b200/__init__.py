@@ -271,7 +271,7 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream():
     """The current stream of the current device, as an address (the raw
     lookup: building torch.cuda.current_stream() costs 3 us a call)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ok(code: int, where: str):
@@ -609,8 +609,8 @@ def device_status(workspace: torch.Tensor) -> int:
 def _call(dev: torch.device, name: str, *args):
     """A library call on the current stream of `dev`, which becomes the
     current device for it."""
-    fn = getattr(lib(), name)
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+    fn = getattr(_lib or lib(), name)
+    if dev.type == "cuda" and dev.index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             _ok(fn(*args, _stream()), name)
     else:
@@ -671,7 +671,7 @@ def embed_fwd(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: fl
     ld_out = D if out is None else _check_rows(out, torch.bfloat16, "out", T, D)
     _on_cuda(ids=ids, weight=weight, out=out, dev_status=dev_status)
     if out is None:
-        out = torch.empty((T, D), dtype=torch.bfloat16, device=weight.device)
+        out = weight.new_empty((T, D))
     _call(weight.device, "dlm_embed_fwd", ctypes.byref(layout), _ptr(ids), _ptr(weight), ld_w, V, D, scale, _ptr(out),
           ld_out, _ptr(dev_status))
     return out
@@ -713,7 +713,7 @@ def embed_bwd(layout: Layout, ids: torch.Tensor, d_out: torch.Tensor, vocab: int
     _on_cuda(ids=ids, d_out=d_out, d_weight=d_weight, workspace=workspace)
     dev = d_out.device
     if d_weight is None:
-        d_weight = torch.empty((vocab, D), dtype=grad_dtype, device=dev)
+        d_weight = d_out.new_empty((vocab, D), dtype=grad_dtype)
     if workspace is None:
         workspace = _aligned_workspace(embed_bwd_workspace_size(layout, D, vocab), dev, 256)
     _call(dev, "dlm_embed_bwd", ctypes.byref(layout), _ptr(ids), _ptr(d_out), ld, vocab, D, scale, gt, int(accumulate),
@@ -837,7 +837,7 @@ def norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optio
         else:
             rstd, mean = torch.empty(rows, dtype=torch.float32, device=dev), None
         pk = _empty_packed(rows, D, pack, dev) if pack != PACK_NONE else None
-        out = NormOut(torch.empty((rows, D), dtype=torch.bfloat16, device=dev), mean, rstd, pk)
+        out = NormOut(x.new_empty((rows, D)), mean, rstd, pk)
     _call(x.device, "dlm_norm_fwd", _ptr(x), rows, D, ld, _ptr(weight), _ptr(bias), pt, kind, eps, weight_offset,
           _ptr(out.y), ld_y, _ptr(out.mean) if layer else None, _ptr(out.rstd), pack,
           _ptr(pk.q) if pk is not None else None, _ptr(pk.scale) if pk is not None else None)
@@ -905,7 +905,7 @@ def norm_bwd(d_y: torch.Tensor, x, rstd: torch.Tensor, mean: Optional[torch.Tens
              d_weight=d_weight, d_bias=d_bias, workspace=workspace)
     dev = d_y.device
     if d_x is None:
-        d_x = torch.empty((rows, D), dtype=torch.bfloat16, device=dev)
+        d_x = d_y.new_empty((rows, D))
     if want_w and want_b and d_weight is None and d_bias is None:
         both = torch.empty((2, D), dtype=grad_dtype, device=dev)
         d_weight, d_bias = both[0], both[1]

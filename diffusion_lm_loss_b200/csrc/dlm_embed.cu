@@ -1,7 +1,7 @@
 // dlm_embed.cu -- token embedding with a scale, and its gradient.
 //
-// Forward: out[i, :] = bf16(scale * W[id_i, :]), one warp per 128 vectors of
-// a token's row.
+// Forward: out[i, :] = bf16(scale * W[id_i, :]), a warp per 1,024 columns of a
+// token's row.
 //
 // Gradient: dW[v, :] = scale * sum over the tokens i with id_i = v of
 // dOut[i, :].  Absorbing noise makes one id (the mask) carry about half of
@@ -24,6 +24,7 @@
 
 #include "dlm_device.cuh"
 #include "dlm_host.h"
+#include "dlm_shift.cuh"
 
 namespace dlm {
 
@@ -40,18 +41,17 @@ constexpr int kJoinWarps = 16;
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <int kVec>
+template <bool kAligned>
 __global__ void __launch_bounds__(kEmbThreads) k_embed_fwd(const int32_t* __restrict__ ids,
                                                            const uint8_t* __restrict__ pad, int64_t n_tokens,
                                                            const uint16_t* __restrict__ w, int64_t ld_w, int vocab,
                                                            int d, float scale, uint16_t* __restrict__ out,
                                                            int64_t ld_out, uint32_t* __restrict__ status) {
-    constexpr int kU = kVec == 8 ? 4 : 16;     // loads in flight per lane
+    constexpr int kU = 4;              // pieces of 8 columns a lane, 256 apart
     pdl_wait();                        // ids come from the corruption kernel
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int nv = d / kVec;
-    const int slabs = (nv + 32 * kU - 1) / (32 * kU);
+    const int slabs = (d + 256 * kU - 1) / (256 * kU);
     const int64_t items = n_tokens * slabs;
     const int64_t step = int64_t(gridDim.x) * (kEmbThreads / 32);
     for (int64_t it = int64_t(blockIdx.x) * (kEmbThreads / 32) + threadIdx.x / 32; it < items; it += step) {
@@ -61,33 +61,27 @@ __global__ void __launch_bounds__(kEmbThreads) k_embed_fwd(const int32_t* __rest
         const int id = is_pad ? -1 : ids[i];
         const bool ok = uint32_t(id) < uint32_t(vocab);
         if (!ok && !is_pad && s == 0 && lane == 0 && status) atomicOr(status, DLM_DEV_BAD_TOKEN_ID);
-        const uint16_t* src = w + int64_t(ok ? id : 0) * ld_w;
-        uint16_t* dst = out + i * ld_out;
-        const int v0 = s * 32 * kU + lane;
-        if constexpr (kVec == 8) {
-            uint4 r[kU];
+        const int c = s * 256 * kU + lane * 8;
+        const uint16_t* src = w + int64_t(ok ? id : 0) * ld_w + c;
+        uint16_t* dst = out + i * ld_out + c;
+        uint4 r[kU];
+        if constexpr (kAligned) {
             #pragma unroll
             for (int u = 0; u < kU; ++u)
-                r[u] = (ok && v0 + 32 * u < nv) ? __ldg(reinterpret_cast<const uint4*>(src) + v0 + 32 * u)
-                                                : make_uint4(0, 0, 0, 0);
-            #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                if (v0 + 32 * u >= nv) break;
-                uint32_t x[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = pack_bf16x2(bf16lo(x[k]) * scale, bf16hi(x[k]) * scale);
-                reinterpret_cast<uint4*>(dst)[v0 + 32 * u] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
+                r[u] = c + 256 * u < d ? __ldg(reinterpret_cast<const uint4*>(src + 256 * u)) : make_uint4(0, 0, 0, 0);
         } else {
-            float r[kU];
-            #pragma unroll
-            for (int u = 0; u < kU; ++u)
-                r[u] = (ok && v0 + 32 * u < nv) ? bf16_bits_to_float(__ldg(src + v0 + 32 * u)) : 0.f;
-            #pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (v0 + 32 * u < nv)
-                    dst[v0 + 32 * u] = __bfloat16_as_ushort(__float2bfloat16_rn(r[u] * scale));
+            load_pieces<kU>(src, c, d, w, w + (vocab - 1) * ld_w + d, r);
         }
+        #pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            uint32_t x[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+            #pragma unroll
+            for (int k = 0; k < 4; ++k)
+                x[k] = ok ? pack_bf16x2(bf16lo(x[k]) * scale, bf16hi(x[k]) * scale) : 0u;
+            r[u] = make_uint4(x[0], x[1], x[2], x[3]);
+            if (kAligned && c + 256 * u < d) *reinterpret_cast<uint4*>(dst + 256 * u) = r[u];
+        }
+        if constexpr (!kAligned) store_pieces<kU>(dst, c, d, r);
     }
 }
 
@@ -145,7 +139,7 @@ __global__ void __launch_bounds__(1024) k_embed_sort(const int32_t* __restrict__
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     const int v0 = blockIdx.x * range;
     const int n = min(range, vocab - v0);
-    for (int k = tid; k < warps * range; k += threads) cnt[k] = 0;
+    for (int k = tid; k < warps * range / 4; k += threads) reinterpret_cast<int4*>(cnt)[k] = make_int4(0, 0, 0, 0);
     if (tid == 0) s_below = 0;
     __syncthreads();
     pdl_wait();
@@ -662,7 +656,7 @@ extern "C" dlm_status_t dlm_embed_fwd(const dlm_layout_t* layout, const int32_t*
                                       int64_t ld_weight, int32_t vocab, int32_t d_model, float scale, uint16_t* out,
                                       int64_t ld_out, uint32_t* dev_status, dlm_stream_t stream) {
     DLM_NVTX("dlm_embed_fwd");
-    if (!layout_ok(layout) || vocab < 1 || d_model < 1 || ld_weight < d_model || ld_out < d_model)
+    if (!layout_ok(layout) || vocab < 1 || d_model < 1 || d_model > INT32_MAX - 1024 || ld_weight < d_model || ld_out < d_model)
         return DLM_ERR_INVALID_ARGUMENT;
     if (!(scale - scale == 0.0f)) return DLM_ERR_INVALID_ARGUMENT;       // inf or NaN
     if (layout->n_tokens == 0) return DLM_OK;
@@ -670,12 +664,10 @@ extern "C" dlm_status_t dlm_embed_fwd(const dlm_layout_t* layout, const int32_t*
     dlm_status_t st = check_device();
     if (st != DLM_OK) return st;
     const bool vec = d_model % 8 == 0 && ld_weight % 8 == 0 && ld_out % 8 == 0 && aligned16(weight) && aligned16(out);
-    const int64_t nv = vec ? d_model / 8 : d_model;
-    const int slab = vec ? 128 : 512;
-    const int64_t items = layout->n_tokens * ((nv + slab - 1) / slab);
+    const int64_t items = layout->n_tokens * ((d_model + 1023) / 1024);
     int64_t blocks = (items + kEmbThreads / 32 - 1) / (kEmbThreads / 32);
     if (blocks > (1 << 20)) blocks = 1 << 20;
-    return launch_pdl(vec ? k_embed_fwd<8> : k_embed_fwd<1>, dim3(unsigned(blocks)), dim3(kEmbThreads), 0,
+    return launch_pdl(vec ? k_embed_fwd<true> : k_embed_fwd<false>, dim3(unsigned(blocks)), dim3(kEmbThreads), 0,
                       (cudaStream_t)stream, "k_embed_fwd launch", ids, layout->pad_mask, layout->n_tokens, weight,
                       ld_weight, vocab, d_model, scale, out, ld_out, dev_status);
 }

@@ -28,13 +28,6 @@ __device__ __forceinline__ PackFactors pack_factors(float amax, int format) {
     return f;
 }
 
-// Code of one element (x = 0 where the block is not finite).
-__device__ __forceinline__ uint32_t pack_code(float x, float inv, int format) {
-    const float u = __fmul_rn(x, inv);
-    if (format == DLM_PACK_INT8) return uint32_t(__float2int_rn(u)) & 0xffu;
-    return uint32_t(__nv_cvt_float_to_fp8(u, __NV_SATFINITE, __NV_E4M3));
-}
-
 __device__ __forceinline__ float unpack_code(uint8_t c, int format) {
     if (format == DLM_PACK_INT8) return float(int8_t(c));
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_fp8_storage_t(c), __NV_E4M3)));
