@@ -28,6 +28,7 @@ Two layers:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -852,6 +853,7 @@ class NormGrad:
     workspace: torch.Tensor       # uint8
 
 
+@functools.lru_cache(maxsize=256)      # of the sizes alone
 def norm_bwd_workspace_size(rows: int, d_model: int) -> int:
     return int(lib().dlm_norm_bwd_workspace_size(rows, d_model))
 

@@ -728,8 +728,7 @@ extern "C" dlm_status_t dlm_embed_bwd(const dlm_layout_t* layout, const int32_t*
     int range = int(align_up(size_t((vocab + 147) / 148), 32));
     if (range > kMaxRange) range = kMaxRange;
     const int warps = range <= kMaxRange / 2 ? 32 : 16;
-    cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSortSmem));
-    if (e != cudaSuccess) { cudaGetLastError(); return cuda_status(e, "k_embed_sort attributes"); }
+    if ((st = allow_smem<k_embed_sort, int(kSortSmem)>("k_embed_sort attributes")) != DLM_OK) return st;
     st = launch_pdl(k_embed_sort, dim3(unsigned((int64_t(vocab) + range - 1) / range)), dim3(unsigned(warps * 32)),
                     size_t(warps) * range * 4, s, "k_embed_sort launch", ids, layout->pad_mask, layout->n_tokens, vocab,
                     range, hdr, row_start, order, sid, int(aligned16(ids)));

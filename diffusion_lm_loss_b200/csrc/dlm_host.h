@@ -2,6 +2,7 @@
 // checks, the device capability check, launch-error mapping.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -64,6 +65,21 @@ inline dlm_status_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, si
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
     if (e != cudaSuccess) cudaGetLastError();
     return cuda_status(e, what);
+}
+
+// Lets a kernel use up to kBytes of dynamic shared memory: asked of the runtime
+// once per kernel and device (one limit per kernel, so that no call lowers
+// another's).
+template <auto kKern, int kBytes>
+inline dlm_status_t allow_smem(const char* what) {
+    static std::atomic<bool> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev >= 0 && dev < 64 && allowed[dev].load(std::memory_order_relaxed)) return DLM_OK;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kKern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) { cudaGetLastError(); return cuda_status(e, what); }
+    if (dev >= 0 && dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
+    return DLM_OK;
 }
 
 // Layout sanity that the host can see (the device checks cu_seqlens itself).

@@ -62,7 +62,9 @@ struct NormBwdArgs {
     int64_t ld_dx;
     float* part;           // [partial rows][2][pitch]: dw, db
     int pitch;
-    int want_dw, want_db;
+    void* d_weight;        // NULL: not wanted
+    void* d_bias;
+    int grad_f32, accumulate;
 };
 
 __device__ __forceinline__ float param_at(const void* p, int f32, int c) {
@@ -84,6 +86,18 @@ __device__ __forceinline__ void load_params(const void* p, int f32, int c, float
         const uint32_t t[4] = {v.x, v.y, v.z, v.w};
         #pragma unroll
         for (int k = 0; k < 4; ++k) { o[2 * k] = bf16lo(t[k]); o[2 * k + 1] = bf16hi(t[k]); }
+    }
+}
+
+// One element of a parameter's gradient (out NULL: not wanted)
+__device__ __forceinline__ void put_grad(void* out, int c, float v, int f32, int accumulate) {
+    if (!out) return;
+    if (f32) {
+        float* o = static_cast<float*>(out) + c;
+        *o = accumulate ? *o + v : v;
+    } else {
+        uint16_t* o = static_cast<uint16_t*>(out) + c;
+        *o = __bfloat16_as_ushort(__float2bfloat16_rn(accumulate ? bf16_bits_to_float(*o) + v : v));
     }
 }
 
@@ -665,8 +679,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
             sw += acc[at];
             sb += acc[at + wide];
         }
-        if (a.want_dw) part[c] = sw;
-        if (a.want_db) part[a.pitch + c] = sb;
+        if (gridDim.x == 1) {                             // the whole sum: no k_norm_join
+            put_grad(a.d_weight, c, sw, a.grad_f32, a.accumulate);
+            put_grad(a.d_bias, c, sb, a.grad_f32, a.accumulate);
+        } else {
+            if (a.d_weight) part[c] = sw;
+            if (a.d_bias) part[a.pitch + c] = sb;
+        }
     }
 }
 
@@ -866,8 +885,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_any(NormBwdArgs a,
     __syncthreads();
     float* part = a.part + int64_t(blockIdx.x) * 2 * a.pitch;
     for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-        if (a.want_dw) part[c] = acc[c];
-        if (a.want_db) part[a.pitch + c] = acc[a.d + c];
+        if (a.d_weight) part[c] = acc[c];
+        if (a.d_bias) part[a.pitch + c] = acc[a.d + c];
     }
 }
 
@@ -940,8 +959,8 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_bwd_wide(NormBwdArgs a) {
             const float g = dy * (a.w ? param_at(a.w, a.param_f32, c) + a.offset : 1.f);
             s1 += g;
             s2 += g * xh;
-            if (a.want_dw) part[c] = (first ? 0.f : part[c]) + dy * xh;
-            if (a.want_db) part[a.pitch + c] = (first ? 0.f : part[a.pitch + c]) + dy;
+            if (a.d_weight) part[c] = (first ? 0.f : part[c]) + dy * xh;
+            if (a.d_bias) part[a.pitch + c] = (first ? 0.f : part[a.pitch + c]) + dy;
         }
         s1 = cta_sum(s1, s);
         s2 = cta_sum(s2, s);
@@ -988,13 +1007,7 @@ __global__ void __launch_bounds__(kNormJoinWarps * 32) k_norm_join(const float* 
     acc = 0.f;
     #pragma unroll
     for (int w = 0; w < kNormJoinWarps; ++w) acc += s[w][lane];
-    if (grad_f32) {
-        float* o = static_cast<float*>(out) + c;
-        *o = accumulate ? *o + acc : acc;
-    } else {
-        uint16_t* o = static_cast<uint16_t*>(out) + c;
-        *o = __bfloat16_as_ushort(__float2bfloat16_rn(accumulate ? bf16_bits_to_float(*o) + acc : acc));
-    }
+    put_grad(out, c, acc, grad_f32, accumulate);
 }
 
 // ---------------------------------------------------------------------------
@@ -1041,22 +1054,29 @@ static RingShape ring_shape(int32_t d, bool shift, int warps, int* pieces) {
     return sh;
 }
 
-template <typename Args>
-static dlm_status_t launch_ring(void (*kern)(Args, RingShape), const Args& a, RingShape sh, int slots, unsigned grid,
-                                cudaStream_t s, const char* what) {
+// kSlots: a thread's 16-byte slots in shared memory
+template <auto kKern, int kSlots, typename Args>
+static dlm_status_t launch_ring(const Args& a, RingShape sh, unsigned grid, cudaStream_t s, const char* what) {
     const unsigned threads = unsigned(sh.nw * sh.groups * 32);
-    const size_t smem = size_t(slots) * threads * 16;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) { cudaGetLastError(); return cuda_status(e, what); }
-    return launch_pdl(kern, dim3(grid), dim3(threads), smem, s, what, a, sh);
+    dlm_status_t st = allow_smem<kKern, kSlots * kRingThreads * 16>(what);
+    if (st != DLM_OK) return st;
+    return launch_pdl(kKern, dim3(grid), dim3(threads), size_t(kSlots) * threads * 16, s, what, a, sh);
+}
+
+template <int kN, bool kShift>
+static dlm_status_t launch_fwd_ring(const NormFwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
+    return launch_ring<k_norm_fwd_ring<kN, kShift>, 2 * kN * kFwdStages>(a, sh, grid, s, "k_norm_fwd launch");
 }
 
 template <int kN, bool kShift>
 static dlm_status_t launch_bwd_ring(const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
-    auto kern = a.format == DLM_PACK_NONE ? k_norm_bwd_ring<kN, DLM_PACK_NONE, kShift>
-              : a.format == DLM_PACK_INT8 ? k_norm_bwd_ring<kN, DLM_PACK_INT8, kShift>
-                                          : k_norm_bwd_ring<kN, DLM_PACK_E4M3, kShift>;
-    return launch_ring(kern, a, sh, 2 * kN * bwd_stages<kN>(), grid, s, "k_norm_bwd launch");
+    constexpr int kSlots = 2 * kN * bwd_stages<kN>();
+    const char* what = "k_norm_bwd launch";
+    if (a.format == DLM_PACK_NONE)
+        return launch_ring<k_norm_bwd_ring<kN, DLM_PACK_NONE, kShift>, kSlots>(a, sh, grid, s, what);
+    if (a.format == DLM_PACK_INT8)
+        return launch_ring<k_norm_bwd_ring<kN, DLM_PACK_INT8, kShift>, kSlots>(a, sh, grid, s, what);
+    return launch_ring<k_norm_bwd_ring<kN, DLM_PACK_E4M3, kShift>, kSlots>(a, sh, grid, s, what);
 }
 
 static unsigned ring_grid(int64_t rows) { return unsigned(rows < 148 ? rows : 148); }
@@ -1078,21 +1098,27 @@ static RingShape any_shape(int32_t d) {
     return sh;
 }
 
-// A slot holds a row's chunks; `acc`: shared memory that the kernel needs
-// besides (its ring is free by then).
-template <typename Args>
-static dlm_status_t launch_any(void (*kern)(Args, RingShape, int), const Args& a, RingShape sh, int tensors, size_t acc,
-                               cudaStream_t s, const char* what) {
+// A slot holds a row's chunks.  16 warps x 512 elements bound what a CTA's
+// groups hold together: 12 slots a group (backward: two tensors) of 2 d + 45
+// bytes at most are 12 x (16 KB + 16 x 45 B); the sums at the end, 8 d, are less.
+constexpr int kAnySmem = 12 * (16 * 1024 + 16 * 45);
+
+template <auto kKern, typename Args>
+static dlm_status_t launch_any(const Args& a, RingShape sh, int tensors, cudaStream_t s, const char* what) {
     const int slot = int(align_up(size_t(a.d) * 2 + 30, 16));
     size_t smem = size_t(sh.groups) * kAnyStages * tensors * slot;
-    if (smem < acc) smem = acc;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) { cudaGetLastError(); return cuda_status(e, what); }
-    return launch_pdl(kern, dim3(ring_grid(a.rows)), dim3(unsigned(sh.nw * sh.groups * 32)), smem, s, what, a, sh, slot);
+    if (smem < size_t(a.d) * 8) smem = size_t(a.d) * 8;
+    dlm_status_t st = allow_smem<kKern, kAnySmem>(what);
+    if (st != DLM_OK) return st;
+    return launch_pdl(kKern, dim3(ring_grid(a.rows)), dim3(unsigned(sh.nw * sh.groups * 32)), smem, s, what, a, sh, slot);
 }
 
 // The backward pass leaves one partial row per CTA, of which there is at most
 // one per SM, whatever the kernel.
+// Up to so many rows a group, one CTA takes them all and writes the gradients
+// itself: its rows, one after the other, take no longer than a second launch.
+constexpr int kAloneRows = 2;
+
 struct NormBwdPlan { unsigned grid; int pitch; size_t bytes; };
 
 static bool norm_bwd_plan(int64_t rows, int32_t d, NormBwdPlan* p) {
@@ -1137,8 +1163,8 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
         const int nv = d_model / 8;
         const int64_t all = rows * nv;                   // 16-byte pieces of the call
         if (sh.nw && all >= kRingPieces && pack_format == DLM_PACK_NONE)
-            return launch_ring(pieces == 1 ? k_norm_fwd_ring<1, false> : k_norm_fwd_ring<2, false>, a, sh,
-                               2 * pieces * kFwdStages, ring_grid(rows), s, "k_norm_fwd launch");
+            return pieces == 1 ? launch_fwd_ring<1, false>(a, sh, ring_grid(rows), s)
+                               : launch_fwd_ring<2, false>(a, sh, ring_grid(rows), s);
         if (all <= kOnePiece && warps_for(nv, 1)) return launch_fwd_vec<1>(warps_for(nv, 1), a, s);
         if (all <= kTwoPieces && warps_for(nv, 2)) return launch_fwd_vec<2>(warps_for(nv, 2), a, s);
         if (warps_for(nv, 4)) return launch_fwd_vec<4>(warps_for(nv, 4), a, s);
@@ -1148,9 +1174,9 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
     sh = ring_shape(d_model, true, kRingThreads / 32, &pieces);
     const RingShape any = any_shape(d_model);
     if (shift && sh.nw)
-        st = launch_ring(pieces == 1 ? k_norm_fwd_ring<1, true> : k_norm_fwd_ring<2, true>, a, sh,
-                         2 * pieces * kFwdStages, shift_grid(rows, sh), s, "k_norm_fwd launch");
-    else if (any.nw) st = launch_any(k_norm_fwd_any, a, any, 1, 0, s, "k_norm_fwd launch");
+        st = pieces == 1 ? launch_fwd_ring<1, true>(a, sh, shift_grid(rows, sh), s)
+                         : launch_fwd_ring<2, true>(a, sh, shift_grid(rows, sh), s);
+    else if (any.nw) st = launch_any<k_norm_fwd_any>(a, any, 1, s, "k_norm_fwd launch");
     else st = launch_pdl(k_norm_fwd_wide, dim3(unsigned(rows < 148 * 4 ? rows : 148 * 4)), dim3(kWideThreads), 0, s,
                          "k_norm_fwd_wide launch", a);
     if (st != DLM_OK || pack_format == DLM_PACK_NONE) return st;
@@ -1190,7 +1216,8 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
     NormBwdArgs a = {d_y, ld_dy, pack_format == DLM_PACK_NONE ? x : nullptr, ld_x, pack_format, q, q_scale, mean,
                      rstd, weight, param_dtype == DLM_F32, kind == DLM_NORM_RMS, weight_offset, rows, d_model, d_x,
                      ld_dx, static_cast<float*>(workspace), p.pitch,
-                     d_weight != nullptr, d_bias != nullptr};
+                     d_weight, d_bias, grad_dtype == DLM_F32, accumulate};
+    bool alone = false;      // one CTA, which writes the gradients itself
     if (rows > 0) {
         const bool vec = d_model % 8 == 0 && ld_dy % 8 == 0 && ld_dx % 8 == 0 && aligned16(d_y) && aligned16(d_x) &&
                          (a.x ? ld_x % 8 == 0 && aligned16(x) : (reinterpret_cast<uintptr_t>(q) & 7) == 0);
@@ -1200,21 +1227,28 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
                                 : (reinterpret_cast<uintptr_t>(q) & 7) == 0 && (ld_dy - d_model) % 8 == 0);
         int pieces = 0;
         const RingShape sh = ring_shape(d_model, !vec, kRingThreads / 32, &pieces), any = any_shape(d_model);
+        const bool ring = (vec || shift) && sh.nw;
+        // (a group's rows are `groups` apart then: in step only if that is a multiple of 8)
+        if (ring && rows <= (vec || sh.groups % 8 == 0 ? int64_t(kAloneRows) * sh.groups : sh.groups)) {
+            p.grid = 1;
+            alone = true;
+        }
         if (vec && sh.nw) {
             st = pieces == 1 ? launch_bwd_ring<1, false>(a, sh, p.grid, s) : launch_bwd_ring<2, false>(a, sh, p.grid, s);
         } else if (shift && sh.nw) {
-            p.grid = shift_grid(rows, sh);
+            if (!alone) p.grid = shift_grid(rows, sh);
             st = pieces == 1 ? launch_bwd_ring<1, true>(a, sh, p.grid, s) : launch_bwd_ring<2, true>(a, sh, p.grid, s);
         } else if (any.nw) {
-            auto kern = pack_format == DLM_PACK_NONE ? k_norm_bwd_any<DLM_PACK_NONE>
-                      : pack_format == DLM_PACK_INT8 ? k_norm_bwd_any<DLM_PACK_INT8> : k_norm_bwd_any<DLM_PACK_E4M3>;
-            st = launch_any(kern, a, any, 2, size_t(d_model) * 8, s, "k_norm_bwd launch");
+            const char* what = "k_norm_bwd launch";
+            st = pack_format == DLM_PACK_NONE ? launch_any<k_norm_bwd_any<DLM_PACK_NONE>>(a, any, 2, s, what)
+               : pack_format == DLM_PACK_INT8 ? launch_any<k_norm_bwd_any<DLM_PACK_INT8>>(a, any, 2, s, what)
+                                              : launch_any<k_norm_bwd_any<DLM_PACK_E4M3>>(a, any, 2, s, what);
         } else {
             st = launch_pdl(k_norm_bwd_wide, dim3(p.grid), dim3(kWideThreads), 0, s, "k_norm_bwd_wide launch", a);
         }
         if (st != DLM_OK) return st;
     }
-    if (!d_weight && !d_bias) return DLM_OK;
+    if ((!d_weight && !d_bias) || alone) return DLM_OK;
     return launch_pdl(k_norm_join, dim3(unsigned((d_model + 31) / 32), 2), dim3(kNormJoinWarps * 32), 0, s,
                       "k_norm_join launch", (const float*)a.part, int(p.grid), p.pitch, d_model,
                       int(grad_dtype == DLM_F32), accumulate, d_weight, d_bias);

@@ -46,7 +46,8 @@ def _check_packed(p, x, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("r,d", [(1, 1), (1, 8), (3, 127), (3, 128), (3, 129), (5, 136), (130, 1001), (2, 4096), (37, 520),
-                                 (1000, 256), (1, 70000), (4099, 24)])
+                                 (1000, 256), (1, 70000), (4099, 24), (50, 1023), (50, 1025),
+                                 (33, 2047), (33, 2049), (17, 7), (200, 5001)])
 def test_pack_and_unpack(r, d, fmt):
     x = _x(r, d, r + d)
     v = _check_packed(dlm.pack8(x, fmt), x, fmt)
@@ -91,7 +92,8 @@ def test_special_blocks(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("d,ld,shift", [(256, 264, 0), (256, 257, 0), (1000, 1000, 4), (129, 136, 8)])
+@pytest.mark.parametrize("d,ld,shift", [(256, 264, 0), (256, 257, 0), (1000, 1000, 4), (129, 136, 8),
+                                         (1030, 1031, 1), (1024, 1024, 3), (2050, 2053, 6)])
 def test_strides(d, ld, shift, fmt):
     x = _x(19, d, d)
     buf = torch.zeros(19 * ld + shift, dtype=bf16, device="cuda")

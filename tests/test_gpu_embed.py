@@ -55,7 +55,8 @@ def _ids(kind, t, vocab, g):
 @pytest.mark.parametrize("t,vocab,d,ldw,ldo,shift", [
     (1, 1, 1, 1, 1, 0), (1, 5, 8, 8, 8, 0), (5, 7, 1001, 1001, 1001, 0), (130, 1024, 256, 256, 256, 0),
     (64, 333, 1000, 1008, 1016, 0), (64, 333, 1000, 1001, 1003, 0), (33, 100, 4096, 4096, 4096, 1),
-    (257, 5000, 4104, 4104, 4104, 0), (700, 50, 24, 24, 24, 0)])
+    (257, 5000, 4104, 4104, 4104, 0), (700, 50, 24, 24, 24, 0), (9, 30, 1023, 1023, 1025, 0), (9, 30, 1025, 1027, 1025, 3),
+    (40, 30, 2047, 2047, 2047, 0), (40, 30, 2049, 2051, 2050, 5), (6, 7, 1024, 1024, 1024, 7), (6, 7, 263, 265, 270, 2)])
 @pytest.mark.parametrize("scale", [1.0, 31.625])
 def test_forward(t, vocab, d, ldw, ldo, shift, scale):
     g = _gen(t + d)
@@ -98,7 +99,11 @@ def test_forward_bad_ids_give_zero_rows_and_a_status_bit():
     (1, 1, 1, "one"), (1, 64, 8, "rand"), (31, 40, 16, "one"), (32, 40, 16, "one"), (33, 40, 16, "one"),
     (64, 40, 8, "last"), (65, 40, 264, "one"), (130, 1024, 256, "masked"), (1000, 2, 72, "rand"),
     (1000, 131, 1000, "runs"), (4097, 1024, 136, "masked"), (5000, 300, 33, "masked"), (777, 5000, 1001, "rand"),
-    (3000, 262144, 8, "masked"), (3000, 300001, 8, "rand"), (20000, 1000, 40, "one"), (100, 20, 9000, "runs")])
+    (3000, 262144, 8, "masked"), (3000, 300001, 8, "rand"), (20000, 1000, 40, "one"), (100, 20, 9000, "runs"),
+    # either side of the single launch's limits (tokens, bytes of the table), and tables whose zeros take every path
+    (1024, 500, 512, "masked"), (1025, 500, 512, "masked"), (1024, 500, 512, "one"), (600, 9000, 1000, "runs"),
+    (600, 9000, 1001, "runs"), (1, 40000, 1001, "rand"), (50, 3000, 9000, "masked"), (2000, 3000, 1500, "runs"),
+    (33, 1000003, 9, "rand"), (40000, 70, 264, "masked")])
 def test_gradient(t, vocab, d, kind, dtype):
     g = _gen(t + vocab + d)
     ids = _ids(kind, t, vocab, g)
@@ -119,7 +124,8 @@ def test_gradient(t, vocab, d, kind, dtype):
 
 @pytest.mark.parametrize("dtype", [bf16, f32])
 @pytest.mark.parametrize("t,vocab,d,ld,ldw,shift", [(200, 64, 40, 48, 56, 0), (200, 64, 40, 41, 43, 0), (97, 33, 128, 128, 128, 1),
-                                                    (500, 40, 1001, 1001, 1001, 0)])
+                                                    (500, 40, 1001, 1001, 1001, 0), (300, 20011, 520, 528, 536, 0),
+                                                    (1500, 20011, 521, 523, 525, 1), (300, 60000, 40, 40, 40, 0)])
 def test_gradient_pads_strides_and_accumulate(t, vocab, d, ld, ldw, shift, dtype):
     g = _gen(d + ld)
     ids = _ids("masked", t, vocab, g)
@@ -172,6 +178,14 @@ def test_gradient_no_tokens_all_pads_bad_ids():
     want = torch.zeros((9, 64), device="cuda")
     want[3], want[8] = dy[0].float(), dy[3].float()
     assert torch.equal(out.d_weight, want)
+    # the same through the three launches of a large table
+    big = dlm.embed_bwd(dlm.make_layout(1, 6), torch.tensor([3, 40000, -1, 8, 2147483647, 39999], dtype=torch.int32, device="cuda"),
+                        _randn((6, 512), g), 40000, grad_dtype=f32)
+    assert big.device_status() == dlm.DEV_BAD_TOKEN_ID
+    assert big.d_weight.any(1).nonzero()[:, 0].tolist() == [3, 8, 39999]
+    empty = dlm.embed_bwd(dlm.make_layout(1, 0), torch.empty(0, dtype=torch.int32, device="cuda"), _randn((0, 512), g), 40000,
+                          d_weight=big.d_weight.fill_(float("nan")), workspace=big.workspace)
+    assert empty.device_status() == 0 and not empty.d_weight.any()
     # the next call on the same workspace reports itself only
     ok = dlm.embed_bwd(dlm.make_layout(1, 1), bad[:1], dy[:1], 9, workspace=out.workspace)
     assert ok.device_status() == 0

@@ -97,6 +97,64 @@ def test_row_counts(r, d):
     _check_bwd(got, dy, x, out.mean, out.rstd, w, False, 0.0, f32)
 
 
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("d", [65, 500, 1501, 2001, 3003, 5001, 8100])
+def test_many_rows_off_the_16_byte_borders(d, fmt):
+    """Rows in step with one another but not with the borders, several to a
+    group of warps, whose rows must keep one phase."""
+    r = 1300 if d > 1000 else 5000
+    x, w, b, dy = _make(r, d, f32 if d % 2 else bf16, 0.0, d + fmt)
+    x[r // 2] = float("inf")                  # a neighbour's infinities stay out
+    out = dlm.norm_fwd(x, w, b, pack=fmt)
+    ok = torch.ones(r, dtype=torch.bool, device="cuda")
+    ok[r // 2] = False
+    sub = dlm.NormOut(out.y[ok], out.mean[ok], out.rstd[ok], None)
+    _check_fwd(sub, x[ok], w, b, 1e-5, False, 0.0)
+    x[r // 2] = 1.0
+    out = dlm.norm_fwd(x, w, b, pack=fmt)
+    got = dlm.norm_bwd(dy, out.packed if fmt else x, out.rstd, out.mean, w, want_d_bias=True, grad_dtype=f32)
+    held = ref.held(*ref.pack(x, fmt), fmt, torch.float64).cuda() if fmt else x
+    _check_bwd(got, dy, held, out.mean, out.rstd, w, False, 0.0, f32)
+
+
+@pytest.mark.parametrize("d,ld", [(1000, 1003), (1001, 1001), (264, 264), (77, 85)])
+@pytest.mark.parametrize("shift", [0, 1, 8])
+@pytest.mark.parametrize("r", [1, 2, 400])
+def test_rows_in_and_out_of_step(r, d, ld, shift):
+    """x, y, dy, dx in one stride (in step), and y, dx in another (out of step)."""
+    x, w, b, dy = _make(r, d, f32, 0.0, ld + shift + r)
+    for other in (ld, ld + 1):
+        xs, dys = _placed(x, ld, shift), _placed(dy, ld, shift)
+        y, dx = _placed(x * 0, other, shift), _placed(x * 0, other, shift)
+        out = dlm.norm_fwd(xs, w, b, out=dlm.NormOut(y, torch.empty(r, device="cuda"), torch.empty(r, device="cuda"), None))
+        _check_fwd(out, x, w, b, 1e-5, False, 0.0)
+        got = dlm.norm_bwd(dys, xs, out.rstd, out.mean, w, want_d_bias=True, d_x=dx, grad_dtype=f32)
+        _check_bwd(got, dy, x, out.mean, out.rstd, w, False, 0.0, f32)
+        for v in (y, dx):
+            v.fill_(7.0)
+            assert bool((v._base == 7.0).all()), "wrote outside its columns"
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("r,d", [(1, 4096), (2, 4096), (4, 4096), (5, 4096), (7, 1001), (16, 256), (32, 256), (33, 256)])
+def test_accumulate_with_few_rows(r, d, dtype):
+    """One CTA that writes the gradients itself, and the first size with two
+    launches, both ways of writing."""
+    x, w, b, dy = _make(r, d, bf16, 0.0, r)
+    out = dlm.norm_fwd(x, w, b)
+    got = dlm.norm_bwd(dy, x, out.rstd, out.mean, w, want_d_bias=True, grad_dtype=dtype)
+    _check_bwd(got, dy, x, out.mean, out.rstd, w, False, 0.0, dtype)
+    old = torch.randn(d, device="cuda").to(dtype)
+    dw, db = old.clone(), old.clone()
+    dlm.norm_bwd(dy, x, out.rstd, out.mean, w, d_weight=dw, d_bias=db, accumulate=True)
+    _, ew, eb = ref.norm_grad(dy, x, out.mean, out.rstd, w, False, 0.0)
+    _, bw, bb = ref.norm_grad_bounds(dy, x, out.mean, out.rstd, w, False, 0.0, f32)
+    for g, e, bound in ((dw, ew, bw), (db, eb, bb)):
+        want = old.double() + e
+        # the sum's own error, one fp32 addition, the output's rounding
+        ref.assert_within(g, want, bound + 1.01 * (ref.HALF[dtype] * want.abs() + ref.U * (want.abs() + bound)))
+
+
 @pytest.mark.parametrize("fmt", [1, 2])
 @pytest.mark.parametrize("kind", [LAYER, RMS])
 @pytest.mark.parametrize("r,d", [(3, 8), (37, 200), (9, 1001), (150, 4096), (300, 520), (5, 8200), (2, 40000), (2, 9001)])

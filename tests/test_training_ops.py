@@ -263,6 +263,9 @@ def test_cuda_failures_are_reported(L):
             _fails_at(L, L.dlm_embed_fwd(p, 256, 512, 64, 100, 64, 1.0, 1024, 64, None, None), "k_embed_fwd launch")
             n = L.dlm_embed_bwd_workspace_size(p, 64, 100)
             _fails_at(L, L.dlm_embed_bwd(p, 256, 512, 64, 100, 64, 1.0, 0, 0, 1024, 64, ws, n, None), "k_embed_small launch")
+            big = 1 << 22                                       # a table too large for the single launch
+            n = L.dlm_embed_bwd_workspace_size(p, 64, big)
+            _fails_at(L, L.dlm_embed_bwd(p, 256, 512, 64, big, 64, 1.0, 0, 0, 1024, 64, ws, n, None), "k_embed_sort")
             _fails_at(L, L.dlm_pack8(256, 4, 128, 128, 1, 512, 1024, None), "k_pack8 launch")
             _fails_at(L, L.dlm_unpack8(256, 512, 4, 128, 2, 1024, 128, None), "k_unpack8 launch")
             for d, step in ((64, "k_norm_fwd launch"), (40001, "k_norm_fwd_wide launch")):
