@@ -656,6 +656,11 @@ def _param_dtype(dtype, name: str) -> int:
     return PARAM_DTYPES[dtype]
 
 
+def _pad_mask(layout: Layout) -> Optional[torch.Tensor]:
+    """The pad mask of a layout from make_layout."""
+    return getattr(layout, "_tensors", (None, None))[1]
+
+
 def embed_fwd(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
               out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """scale * weight[ids] as bf16 [n_tokens, d_model] (see dlm_embed_fwd);
@@ -670,7 +675,7 @@ def embed_fwd(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: fl
     if dev_status is not None and (dev_status.dtype not in (torch.int32, torch.uint32) or dev_status.numel() < 1):
         raise ValueError("dev_status: an int32 / uint32 tensor of at least one element")
     ld_out = D if out is None else _check_rows(out, torch.bfloat16, "out", T, D)
-    _on_cuda(ids=ids, weight=weight, out=out, dev_status=dev_status)
+    _on_cuda(ids=ids, weight=weight, out=out, dev_status=dev_status, pad_mask=_pad_mask(layout))
     if out is None:
         out = weight.new_empty((T, D))
     _call(weight.device, "dlm_embed_fwd", ctypes.byref(layout), _ptr(ids), _ptr(weight), ld_w, V, D, scale, _ptr(out),
@@ -711,7 +716,7 @@ def embed_bwd(layout: Layout, ids: torch.Tensor, d_out: torch.Tensor, vocab: int
     ld_dw = D if d_weight is None else _check_rows(d_weight, grad_dtype, "d_weight", vocab, D)
     if workspace is not None:
         _check(workspace, torch.uint8, "workspace", min_numel=0)
-    _on_cuda(ids=ids, d_out=d_out, d_weight=d_weight, workspace=workspace)
+    _on_cuda(ids=ids, d_out=d_out, d_weight=d_weight, workspace=workspace, pad_mask=_pad_mask(layout))
     dev = d_out.device
     if d_weight is None:
         d_weight = d_out.new_empty((vocab, D), dtype=grad_dtype)
@@ -1089,7 +1094,10 @@ class _EmbedFn(torch.autograd.Function):
 
 def embed(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
     """embed_fwd as a differentiable function of `weight`; its gradient is
-    dense, bf16 [vocab, d_model] (embed_bwd can add it to another one)."""
+    dense, bf16 [vocab, d_model] (embed_bwd can add it to another one).
+    To capture a whole backward pass in a CUDA graph, drop every earlier eager
+    graph of the same parameters first (torch's own rule), or capture embed_bwd
+    and norm_bwd, which have no such state."""
     return _EmbedFn.apply(weight, layout, ids, scale)
 
 

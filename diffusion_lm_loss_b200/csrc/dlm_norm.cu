@@ -1122,7 +1122,7 @@ constexpr int kAloneRows = 2;
 struct NormBwdPlan { unsigned grid; int pitch; size_t bytes; };
 
 static bool norm_bwd_plan(int64_t rows, int32_t d, NormBwdPlan* p) {
-    if (rows < 0 || d < 1 || d > INT32_MAX - 1024) return false;
+    if (rows < 0 || rows > INT32_MAX || d < 1 || d > INT32_MAX - 1024) return false;
     p->grid = ring_grid(rows);
     p->pitch = int(align_up(size_t(d), 32));
     p->bytes = align_up((size_t(p->grid) * 2 + 1) * size_t(p->pitch) * 4, kWsAlign);
@@ -1139,7 +1139,7 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
                                      float* rstd, int32_t pack_format, uint8_t* q, float* q_scale,
                                      dlm_stream_t stream) {
     DLM_NVTX("dlm_norm_fwd");
-    if (rows < 0 || d_model < 1 || d_model > INT32_MAX - 1024 || ld_x < d_model || ld_y < d_model)
+    if (rows < 0 || rows > INT32_MAX || d_model < 1 || d_model > INT32_MAX - 1024 || ld_x < d_model || ld_y < d_model)
         return DLM_ERR_INVALID_ARGUMENT;
     if (kind != DLM_NORM_LAYER && kind != DLM_NORM_RMS) return DLM_ERR_INVALID_ARGUMENT;
     if (param_dtype != DLM_BF16 && param_dtype != DLM_F32) return DLM_ERR_INVALID_ARGUMENT;
@@ -1149,7 +1149,6 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
     if (rows == 0) return DLM_OK;
     if (!x || !y || !rstd || (kind == DLM_NORM_LAYER && !mean)) return DLM_ERR_INVALID_ARGUMENT;
     if (pack_format != DLM_PACK_NONE && (!q || !q_scale)) return DLM_ERR_INVALID_ARGUMENT;
-    if (rows > INT32_MAX) return DLM_ERR_INVALID_ARGUMENT;
     dlm_status_t st = check_device();
     if (st != DLM_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;

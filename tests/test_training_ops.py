@@ -90,7 +90,7 @@ def test_norm_rejections(L):
             rows=4, d=64, dx=16, ld_dx=64, gt=0, acc=0, dw=16, db=16, ws=256, n=need):
         return L.dlm_norm_bwd(dy, ld_dy, x, ld_x, fmt, q, qs, mean, rstd, w, pt, kind, off, rows, d, dx, ld_dx, gt, acc,
                               dw, db, ws, n, None)
-    for kw in (dict(dy=None), dict(ld_dy=63), dict(x=None), dict(ld_x=63), dict(fmt=3), dict(fmt=1, q=16),
+    for kw in (dict(rows=2 ** 31), dict(dy=None), dict(ld_dy=63), dict(x=None), dict(ld_x=63), dict(fmt=3), dict(fmt=1, q=16),
                dict(fmt=1, qs=16), dict(mean=None), dict(rstd=None), dict(pt=2), dict(kind=-1), dict(off=nan),
                dict(rows=-1), dict(d=0), dict(dx=None), dict(ld_dx=63), dict(gt=2), dict(acc=2), dict(ws=None),
                dict(ws=100)):
