@@ -13,7 +13,7 @@
 //                  range, counted in the same pass, give the offset): no
 //                  communication between CTAs, and an order that depends on
 //                  the ids alone.
-//   k_embed_grad   one CTA per kChunk sorted positions and column tile adds
+//   k_embed_grad   one CTA per 8 to 32 sorted positions and column tile adds
 //                  rows in that order, in fp32 registers; a row that begins
 //                  and ends inside the chunk is written at once, a row that
 //                  crosses a chunk's border leaves one fp32 partial per chunk.
@@ -29,7 +29,10 @@
 namespace dlm {
 
 constexpr int kEmbThreads = 256;
-constexpr int kChunk = 32;             // sorted positions per CTA: one per lane
+// Sorted positions per CTA (at most one per lane): 32, or fewer until the call
+// has 16 warps per SM -- with few warps the chunks' rows, read one batch after
+// the other, set the time (5,000 tokens of 1,001 columns: see DESIGN).
+constexpr int kMaxChunk = 32, kMinChunk = 8;
 // Vocabulary rows per sorting CTA: one CTA per SM up to 265,216 rows.  A
 // counter for each row and warp: 32 warps with up to 896 rows, 16 with more
 // (112 KB either way).
@@ -288,6 +291,7 @@ struct EmbGradArgs {
     const int32_t* sid;
     float* part;          // [chunks][2][pitch]: 0 = rows begun before the chunk, 1 = the row that goes on behind it
     int pitch;
+    int chunk;            // sorted positions per CTA of k_embed_grad
     int tiles;            // column tiles of a row in k_embed_grad
     int64_t n_tokens;
     int64_t chunk_ctas;   // k_embed_grad's CTAs that add up; those behind them write zeros
@@ -327,10 +331,14 @@ __device__ __forceinline__ void zero_rows(const EmbGradArgs& a, int64_t cta, int
     }
 }
 
-template <int kVec, typename GT>
+// kAligned: rows of d_out and d_weight on 16-byte borders.  Otherwise d_out is
+// read as dlm_shift.cuh does, and a finished row is written by single elements
+// side by side, through a warp's 1 KB of shared memory.
+template <bool kAligned, typename GT>
 __global__ void __launch_bounds__(kGradThreads) k_embed_grad(EmbGradArgs a) {
-    constexpr int kU = 8;                      // rows in flight
-    const int lane = threadIdx.x & 31;
+    constexpr int kU = kAligned ? 8 : 4;       // rows in flight
+    extern __shared__ float s_rows[];          // not kAligned: [warp][256]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
     if (int64_t(blockIdx.x) >= a.chunk_ctas) {
@@ -339,48 +347,73 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(EmbGradArgs a) {
     }
     GT* dw = static_cast<GT*>(a.d_weight);
     const int64_t c = blockIdx.x / a.tiles;
-    const int col = (int(blockIdx.x - c * a.tiles) * blockDim.x + threadIdx.x) * kVec;
+    const int col = (int(blockIdx.x - c * a.tiles) * blockDim.x + threadIdx.x) * 8;
     const bool active = col < a.d;
-    const int64_t p0 = c * kChunk;
+    const int64_t p0 = c * a.chunk;
     const int64_t total = a.row_start[a.vocab];
-    const int n = int(min(int64_t(kChunk), total - p0));
+    const int n = int(min(int64_t(a.chunk), total - p0));
     if (n <= 0) return;
     const int tok = lane < n ? a.order[p0 + lane] : 0;
     const int row = lane < n ? a.sid[p0 + lane] : -1;
     const int before = p0 > 0 ? a.sid[p0 - 1] : -1;
     const int after = p0 + n < total ? a.sid[p0 + n] : -1;
     bool open = before == __shfl_sync(~0u, row, 0);      // the current row began before this chunk
-    float acc[kVec];
+    float acc[8];
     #pragma unroll
-    for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
+    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
     float* part = a.part + (c * 2) * int64_t(a.pitch) + col;
-    const uint16_t* column = a.d_out + (active ? col : 0);
+    const uint16_t* column = a.d_out + (kAligned && !active ? 0 : col);
+    const uint16_t* end = a.d_out + (a.n_tokens - 1) * a.ld + a.d;
     for (int p = 0; p < n; p += kU) {
-        uint4 q[kU];
+        uint4 q[kU], more[kU];                 // more: the chunk behind the last lane's
+        int sh[kU];
         #pragma unroll
-        for (int u = 0; u < kU; ++u)
-            q[u] = load_piece<kVec>(column + __shfl_sync(~0u, tok, min(p + u, n - 1)) * a.ld);
+        for (int u = 0; u < kU; ++u) {
+            const uint16_t* at = column + __shfl_sync(~0u, tok, min(p + u, n - 1)) * a.ld;
+            if constexpr (kAligned) {
+                q[u] = load_piece<8>(at);
+            } else {
+                sh[u] = int(reinterpret_cast<uintptr_t>(at) & 15) / 2;
+                q[u] = col - sh[u] < a.d ? load_chunk(at - sh[u], a.d_out, end) : make_uint4(0, 0, 0, 0);
+                more[u] = make_uint4(0, 0, 0, 0);
+                if (lane == 31 && sh[u] && col + 8 - sh[u] < a.d) more[u] = load_chunk(at + 8 - sh[u], a.d_out, end);
+            }
+        }
         #pragma unroll
         for (int u = 0; u < kU; ++u) {
             if (p + u >= n) break;
-            add_piece<kVec>(q[u], acc);
+            if (!kAligned && sh[u]) {
+                const uint4 next = shfl(q[u], (lane + 1) & 31);
+                q[u] = funnel16(q[u], lane == 31 ? more[u] : next, sh[u]);
+            }
+            add_piece<8>(q[u], acc);
             const int id = __shfl_sync(~0u, row, p + u);
             const int nx = __shfl_sync(~0u, row, (p + u + 1) & 31);
             const bool last = p + u + 1 == n;
             const int next = last ? after : nx;
             if (id != next || last) {
-                if (active) {
-                    if (open || id == next) {            // crosses a border: fp32 partial
-                        float* dst = part + (open ? 0 : a.pitch);
-                        #pragma unroll
-                        for (int k = 0; k < kVec; ++k) dst[k] = acc[k];
-                    } else {
-                        put_row<kVec, GT>(dw + int64_t(id) * a.ld_dw + col, acc, a.scale, a.accumulate);
+                if (open || id == next) {                // crosses a border: fp32 partial
+                    float* dst = part + (open ? 0 : a.pitch);
+                    #pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (kAligned ? active : col + k < a.d) dst[k] = acc[k];
+                } else if constexpr (kAligned) {
+                    if (active) put_row<8, GT>(dw + int64_t(id) * a.ld_dw + col, acc, a.scale, a.accumulate);
+                } else {
+                    __syncwarp();
+                    #pragma unroll
+                    for (int k = 0; k < 8; ++k) s_rows[warp * 256 + lane * 8 + k] = acc[k];
+                    __syncwarp();
+                    #pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int at = lane + 32 * k, cc = col - lane * 8 + at;
+                        const float v[1] = {s_rows[warp * 256 + at]};
+                        if (cc < a.d) put_row<1, GT>(dw + int64_t(id) * a.ld_dw + cc, v, a.scale, a.accumulate);
                     }
                 }
                 open = false;
                 #pragma unroll
-                for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
+                for (int k = 0; k < 8; ++k) acc[k] = 0.f;
             }
         }
     }
@@ -393,7 +426,7 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(EmbGradArgs a) {
 constexpr int kJoinCols = 128;
 
 template <typename GT>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_embed_join(EmbGradArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) k_embed_join(EmbGradArgs a) {
     __shared__ float4 s[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
@@ -407,13 +440,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_embed_join(EmbGradArgs a) {
     const int64_t total = a.row_start[a.vocab];
     {
         int last = 0, row = -1;
-        const int64_t behind = (c0 + lane + 1) * kChunk;
+        const int64_t behind = (c0 + lane + 1) * a.chunk;
         if (behind < n_tokens) {
             // read before `total` is known; meaningless behind it, and then not used as an index
             const int v = a.sid[behind - 1], w = a.sid[behind];
-            if (behind < total && v == w && a.row_start[v] >= behind - kChunk) {
+            if (behind < total && v == w && a.row_start[v] >= behind - a.chunk) {
                 row = v;
-                last = (a.row_start[v + 1] - 1) / kChunk;
+                last = (a.row_start[v + 1] - 1) / a.chunk;
             }
         }
         uint32_t m = __ballot_sync(~0u, row >= 0);
@@ -631,6 +664,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) k_embed_small(EmbSmallArgs a
 // Workspace of the gradient: header, row_start [vocab + 1], order and sid
 // [n_tokens], partials.
 struct EmbPlan {
+    int chunk;
     int64_t chunks;
     int pitch;
     size_t off_start, off_order, off_sid, off_part, bytes;
@@ -638,7 +672,9 @@ struct EmbPlan {
 
 static bool embed_plan(const dlm_layout_t* L, int32_t vocab, int32_t d, EmbPlan* p) {
     if (!layout_ok(L) || vocab < 1 || d < 1 || vocab == INT32_MAX || d > INT32_MAX - 64) return false;
-    p->chunks = (L->n_tokens + kChunk - 1) / kChunk;
+    p->chunk = kMaxChunk;
+    while (p->chunk > kMinChunk && L->n_tokens / p->chunk * ((int64_t(d) + 255) / 256) < 148 * 16) p->chunk /= 2;
+    p->chunks = (L->n_tokens + p->chunk - 1) / p->chunk;
     p->pitch = int(align_up(size_t(d), 32));
     p->off_start = kWsAlign;
     p->off_order = align_up(p->off_start + (size_t(vocab) + 1) * 4, kWsAlign);
@@ -692,7 +728,7 @@ extern "C" dlm_status_t dlm_embed_bwd(const dlm_layout_t* layout, const int32_t*
     if (workspace_bytes < p.bytes) return DLM_ERR_WORKSPACE_TOO_SMALL;
     const bool f32 = grad_dtype == DLM_F32;
     const bool vec = d_model % 8 == 0 && ld % 8 == 0 && ld_dw % 8 == 0 && aligned16(d_out) && aligned16(d_weight);
-    const int nv = vec ? d_model / 8 : d_model;
+    const int nv = (d_model + 7) / 8;
     const unsigned threads = nv >= kGradThreads ? kGradThreads : unsigned(align_up(size_t(nv), 32));
     const int tiles = int((unsigned(nv) + threads - 1) / threads);
     const int join_tiles = (d_model + kJoinCols - 1) / kJoinCols;
@@ -738,13 +774,13 @@ extern "C" dlm_status_t dlm_embed_bwd(const dlm_layout_t* layout, const int32_t*
     a.d_out = d_out; a.ld = ld; a.vocab = vocab; a.d = d_model; a.scale = scale; a.accumulate = accumulate;
     a.d_weight = d_weight; a.ld_dw = ld_dw; a.row_start = row_start; a.order = order; a.sid = sid;
     a.part = reinterpret_cast<float*>(ws + p.off_part);
-    a.pitch = p.pitch; a.tiles = tiles; a.n_tokens = layout->n_tokens; a.chunk_ctas = p.chunks * tiles;
+    a.pitch = p.pitch; a.chunk = p.chunk; a.tiles = tiles; a.n_tokens = layout->n_tokens; a.chunk_ctas = p.chunks * tiles;
     a.join_ctas = join_ctas; a.join_tiles = join_tiles; a.zero_rows = zero_rows; a.zero_split = zero_split;
     if (a.chunk_ctas + zero_grad > 0) {
-        auto kern = f32 ? (vec ? k_embed_grad<8, float> : k_embed_grad<1, float>)
-                        : (vec ? k_embed_grad<8, uint16_t> : k_embed_grad<1, uint16_t>);
-        st = launch_pdl(kern, dim3(unsigned(a.chunk_ctas + zero_grad)), dim3(threads), 0, s,
-                        "k_embed_grad launch", a);
+        auto kern = f32 ? (vec ? k_embed_grad<true, float> : k_embed_grad<false, float>)
+                        : (vec ? k_embed_grad<true, uint16_t> : k_embed_grad<false, uint16_t>);
+        st = launch_pdl(kern, dim3(unsigned(a.chunk_ctas + zero_grad)), dim3(threads), vec ? 0 : threads * 8 * sizeof(float),
+                        s, "k_embed_grad launch", a);
         if (st != DLM_OK) return st;
     }
     if (join_ctas == 0) return DLM_OK;
