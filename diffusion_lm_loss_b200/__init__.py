@@ -607,15 +607,24 @@ def device_status(workspace: torch.Tensor) -> int:
 # --------------------------------------------------------------------------
 # embedding, norm, activations in 8 bits
 # --------------------------------------------------------------------------
-def _call(dev: torch.device, name: str, *args):
-    """A library call on the current stream of `dev`, which becomes the
-    current device for it."""
+def _call(dev: int, name: str, *args):
+    """A library call on the current stream of CUDA device `dev`, which becomes
+    the current device for it (-1: of the current one)."""
     fn = getattr(_lib or lib(), name)
-    if dev.type == "cuda" and dev.index != torch._C._cuda_getDevice():
+    if dev >= 0 and dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             _ok(fn(*args, _stream()), name)
     else:
         _ok(fn(*args, _stream()), name)
+
+
+def _all_on(dev: int, *tensors) -> bool:
+    """Whether these (None = not given) are on CUDA device `dev`: the quick
+    form of _on_cuda, which words what is wrong where it is not so."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            return False
+    return dev >= 0
 
 
 def _check_rows(t: Optional[torch.Tensor], dtype, name: str, rows: int, cols: int) -> int:
@@ -668,18 +677,20 @@ def embed_fwd(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: fl
     DEV_BAD_TOKEN_ID or'ed in when an id is outside the table."""
     T = layout.n_tokens
     _check(ids, torch.int32, "ids", min_numel=T)
-    if weight.dim() != 2 or weight.shape[0] < 1 or weight.shape[1] < 1:
+    V, D = weight.shape if weight.dim() == 2 else (0, 0)
+    if V < 1 or D < 1:
         raise ValueError("weight: [vocab, d_model]")
-    V, D = weight.shape
     ld_w = _check_rows(weight, torch.bfloat16, "weight", V, D)
     if dev_status is not None and (dev_status.dtype not in (torch.int32, torch.uint32) or dev_status.numel() < 1):
         raise ValueError("dev_status: an int32 / uint32 tensor of at least one element")
     ld_out = D if out is None else _check_rows(out, torch.bfloat16, "out", T, D)
-    _on_cuda(ids=ids, weight=weight, out=out, dev_status=dev_status, pad_mask=_pad_mask(layout))
+    dev, pad = weight.get_device(), _pad_mask(layout)
+    if not _all_on(dev, ids, out, dev_status, pad):
+        _on_cuda(ids=ids, weight=weight, out=out, dev_status=dev_status, pad_mask=pad)
     if out is None:
         out = weight.new_empty((T, D))
-    _call(weight.device, "dlm_embed_fwd", ctypes.byref(layout), _ptr(ids), _ptr(weight), ld_w, V, D, scale, _ptr(out),
-          ld_out, _ptr(dev_status))
+    _call(dev, "dlm_embed_fwd", ctypes.byref(layout), ids.data_ptr(), weight.data_ptr(), ld_w, V, D, scale,
+          out.data_ptr(), ld_out, _ptr(dev_status))
     return out
 
 
@@ -716,14 +727,15 @@ def embed_bwd(layout: Layout, ids: torch.Tensor, d_out: torch.Tensor, vocab: int
     ld_dw = D if d_weight is None else _check_rows(d_weight, grad_dtype, "d_weight", vocab, D)
     if workspace is not None:
         _check(workspace, torch.uint8, "workspace", min_numel=0)
-    _on_cuda(ids=ids, d_out=d_out, d_weight=d_weight, workspace=workspace, pad_mask=_pad_mask(layout))
-    dev = d_out.device
+    dev, pad = d_out.get_device(), _pad_mask(layout)
+    if not _all_on(dev, ids, d_weight, workspace, pad):
+        _on_cuda(ids=ids, d_out=d_out, d_weight=d_weight, workspace=workspace, pad_mask=pad)
     if d_weight is None:
         d_weight = d_out.new_empty((vocab, D), dtype=grad_dtype)
     if workspace is None:
-        workspace = _aligned_workspace(embed_bwd_workspace_size(layout, D, vocab), dev, 256)
-    _call(dev, "dlm_embed_bwd", ctypes.byref(layout), _ptr(ids), _ptr(d_out), ld, vocab, D, scale, gt, int(accumulate),
-          _ptr(d_weight), ld_dw, _ptr(workspace), workspace.numel())
+        workspace = _aligned_workspace(embed_bwd_workspace_size(layout, D, vocab), d_out.device, 256)
+    _call(dev, "dlm_embed_bwd", ctypes.byref(layout), ids.data_ptr(), d_out.data_ptr(), ld, vocab, D, scale, gt,
+          int(accumulate), d_weight.data_ptr(), ld_dw, workspace.data_ptr(), workspace.numel())
     return EmbedGrad(d_weight, workspace)
 
 
@@ -765,23 +777,27 @@ def pack8(x: torch.Tensor, format: int = PACK_INT8, out: Optional[Packed8] = Non
             raise ValueError("out: has another format")
     elif format not in (PACK_INT8, PACK_E4M3):
         raise ValueError("format: PACK_INT8 or PACK_E4M3")
-    _on_cuda(x=x, q=out.q if out is not None else None, scale=out.scale if out is not None else None)
+    dev = x.get_device()
+    if not (_all_on(dev) if out is None else _all_on(dev, out.q, out.scale)):
+        _on_cuda(x=x, q=out.q if out is not None else None, scale=out.scale if out is not None else None)
     if out is None:
         out = _empty_packed(rows, cols, format, x.device)
-    _call(x.device, "dlm_pack8", _ptr(x), rows, cols, ld, format, _ptr(out.q), _ptr(out.scale))
+    _call(dev, "dlm_pack8", x.data_ptr(), rows, cols, ld, format, out.q.data_ptr(), out.scale.data_ptr())
     return out
 
 
 def unpack8(packed: Packed8, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The bf16 values that pack8's (or norm_fwd's) codes stand for."""
-    _check(packed.q, torch.uint8, "packed.q", min_rows=0)
-    rows, cols = packed.q.shape
+    rows, cols = _shape2(packed.q, "packed.q")
     _check_packed(packed, rows, cols, "packed")
     ld = cols if out is None else _check_rows(out, torch.bfloat16, "out", rows, cols)
-    _on_cuda(q=packed.q, scale=packed.scale, out=out)
+    dev = packed.q.get_device()
+    if not _all_on(dev, packed.scale, out):
+        _on_cuda(q=packed.q, scale=packed.scale, out=out)
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=packed.q.device)
-    _call(packed.q.device, "dlm_unpack8", _ptr(packed.q), _ptr(packed.scale), rows, cols, packed.format, _ptr(out), ld)
+        out = packed.q.new_empty((rows, cols), dtype=torch.bfloat16)
+    _call(dev, "dlm_unpack8", packed.q.data_ptr(), packed.scale.data_ptr(), rows, cols, packed.format, out.data_ptr(),
+          ld)
     return out
 
 
@@ -835,18 +851,14 @@ def norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optio
         _on_cuda(x=x, weight=weight, bias=bias, y=out.y, mean=out.mean if layer else None, rstd=out.rstd,
                  q=pk.q if pk is not None else None, scale=pk.scale if pk is not None else None)
     else:
-        _on_cuda(x=x, weight=weight, bias=bias)
-        dev = x.device
-        if layer:
-            stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
-            rstd, mean = stats[0], stats[1]
-        else:
-            rstd, mean = torch.empty(rows, dtype=torch.float32, device=dev), None
-        pk = _empty_packed(rows, D, pack, dev) if pack != PACK_NONE else None
-        out = NormOut(x.new_empty((rows, D)), mean, rstd, pk)
-    _call(x.device, "dlm_norm_fwd", _ptr(x), rows, D, ld, _ptr(weight), _ptr(bias), pt, kind, eps, weight_offset,
-          _ptr(out.y), ld_y, _ptr(out.mean) if layer else None, _ptr(out.rstd), pack,
-          _ptr(pk.q) if pk is not None else None, _ptr(pk.scale) if pk is not None else None)
+        if not _all_on(x.get_device(), weight, bias):
+            _on_cuda(x=x, weight=weight, bias=bias)
+        pk = _empty_packed(rows, D, pack, x.device) if pack != PACK_NONE else None
+        out = NormOut(x.new_empty((rows, D)), x.new_empty(rows, dtype=torch.float32) if layer else None,
+                      x.new_empty(rows, dtype=torch.float32), pk)
+    _call(x.get_device(), "dlm_norm_fwd", x.data_ptr(), rows, D, ld, _ptr(weight), _ptr(bias), pt, kind, eps,
+          weight_offset, out.y.data_ptr(), ld_y, out.mean.data_ptr() if layer else None, out.rstd.data_ptr(), pack,
+          pk.q.data_ptr() if pk is not None else None, pk.scale.data_ptr() if pk is not None else None)
     return out
 
 
@@ -893,7 +905,7 @@ def norm_bwd(d_y: torch.Tensor, x, rstd: torch.Tensor, mean: Optional[torch.Tens
     want_w, want_b = want_d_weight or d_weight is not None, want_d_bias or d_bias is not None
     if accumulate and (want_w and d_weight is None or want_b and d_bias is None):
         raise ValueError("accumulate needs d_weight and d_bias for the gradients asked for")
-    for t, name in ((d_weight, "d_weight"), (d_bias, "d_bias")):
+    for t, name in ((d_weight, "d_weight"), (d_bias, "d_bias")) if d_weight is not None or d_bias is not None else ():
         if t is not None:
             _param_dtype(t.dtype, name)
             _check(t, t.dtype, name, min_numel=0)
@@ -908,23 +920,22 @@ def norm_bwd(d_y: torch.Tensor, x, rstd: torch.Tensor, mean: Optional[torch.Tens
     ld_dx = D if d_x is None else _check_rows(d_x, torch.bfloat16, "d_x", rows, D)
     if workspace is not None:
         _check(workspace, torch.uint8, "workspace", min_numel=0)
-    _on_cuda(d_y=d_y, x=xs, q=q, scale=qs, mean=mean if layer else None, rstd=rstd, weight=weight, d_x=d_x,
-             d_weight=d_weight, d_bias=d_bias, workspace=workspace)
-    dev = d_y.device
+    dev = d_y.get_device()
+    if not _all_on(dev, xs, q, qs, mean if layer else None, rstd, weight, d_x, d_weight, d_bias, workspace):
+        _on_cuda(d_y=d_y, x=xs, q=q, scale=qs, mean=mean if layer else None, rstd=rstd, weight=weight, d_x=d_x,
+                 d_weight=d_weight, d_bias=d_bias, workspace=workspace)
     if d_x is None:
         d_x = d_y.new_empty((rows, D))
-    if want_w and want_b and d_weight is None and d_bias is None:
-        both = torch.empty((2, D), dtype=grad_dtype, device=dev)
-        d_weight, d_bias = both[0], both[1]
     if want_w and d_weight is None:
-        d_weight = torch.empty(D, dtype=grad_dtype, device=dev)
+        d_weight = d_y.new_empty(D, dtype=grad_dtype)
     if want_b and d_bias is None:
-        d_bias = torch.empty(D, dtype=grad_dtype, device=dev)
+        d_bias = d_y.new_empty(D, dtype=grad_dtype)
     if workspace is None:
-        workspace = _aligned_workspace(norm_bwd_workspace_size(rows, D), dev, 256)
-    _call(dev, "dlm_norm_bwd", _ptr(d_y), ld_dy, _ptr(xs), ld_x, fmt, _ptr(q), _ptr(qs),
-          _ptr(mean) if layer else None, _ptr(rstd), _ptr(weight), pt, kind, weight_offset, rows, D, _ptr(d_x), ld_dx,
-          gt, int(accumulate), _ptr(d_weight), _ptr(d_bias), _ptr(workspace), workspace.numel())
+        workspace = _aligned_workspace(norm_bwd_workspace_size(rows, D), d_y.device, 256)
+    _call(dev, "dlm_norm_bwd", d_y.data_ptr(), ld_dy, _ptr(xs), ld_x, fmt, _ptr(q), _ptr(qs),
+          mean.data_ptr() if layer else None, rstd.data_ptr(), _ptr(weight), pt, kind, weight_offset, rows, D,
+          d_x.data_ptr(), ld_dx, gt, int(accumulate), _ptr(d_weight), _ptr(d_bias), workspace.data_ptr(),
+          workspace.numel())
     return NormGrad(d_x, d_weight, d_bias, workspace)
 
 

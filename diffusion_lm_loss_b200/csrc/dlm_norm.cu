@@ -7,6 +7,16 @@
 //   dx = rstd (g - mean(g) - xh mean(g xh))     (RMS: without mean(g))
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 //
+// Both passes read and write each row once (4 and 6 bytes an element) and
+// should be bound by HBM.  What has to be kept small beside that is the
+// instructions per element (packed fp32 pairs, parameters in registers) and
+// the exchanges per row.  Measured at 16,384 x 4,096 with weight and bias:
+// forward 47 us (0.87 of the copy rate; one warp group per row without a ring
+// 52, per row of one warp 105), backward 71 us (0.86; one row per CTA of 16
+// warps with plain loads 194), forward that also writes the checkpoint 65 us
+// (0.79, issue-bound: the codes double the instructions), backward from it 76
+// (0.68, bound by its instructions' latency at 16 warps an SM).
+//
 // Many rows on 16-byte borders (k_norm_fwd_ring, k_norm_bwd_ring): one CTA of
 // up to 16 warps per SM, split into groups that each hold a whole row; a group
 // walks over its rows while asynchronous copies fill a ring of the next ones
@@ -135,7 +145,8 @@ __device__ __forceinline__ uint32_t f2to_bf16(uint64_t v) {
 constexpr int groups_per_cta(int nw) { return nw >= 4 ? 1 : 4 / nw; }
 
 // ---------------------------------------------------------------------------
-// forward: a row in the registers of kNW warps, kN pieces of kVec elements a lane
+// forward, one row per group: in the registers of kNW warps, kN pieces of 8
+// elements a lane
 // ---------------------------------------------------------------------------
 template <int kN, int kNW>
 __global__ void __launch_bounds__(kNW * groups_per_cta(kNW) * 32) k_norm_fwd_vec(NormFwdArgs a) {
@@ -230,7 +241,6 @@ constexpr int kRingThreads = 512;
 // lane, `groups` of them make a CTA.
 struct RingShape { int nw, groups; };
 
-
 // The sums of s1 and s2 over a group, in every lane.  Lanes 0..15 carry s1,
 // 16..31 s2.  slot: [nw] float2 that no earlier exchange still reads; `bar`:
 // the group's barrier.
@@ -278,17 +288,9 @@ __device__ __forceinline__ void param_pairs(const void* p, int f32, int c, float
     for (int k = 0; k < 4; ++k) o[k] = f2pack(v[2 * k] + add, v[2 * k + 1] + add);
 }
 
+// Stages of the rings: with one or two pieces a lane 80 or 160 KB (forward), 164
+// or 197 KB (backward) of shared memory, all but one stage of it in flight.
 constexpr int kFwdStages = 5;
-// Which forward kernel, by the call's 16-byte pieces (rows x d / 8).  The fewer,
-// the more warps share a row, so that one row's time, not the bandwidth,
-// counts less; the ring pays once its start is spread over enough rows.
-// Measured (us), d = 4,096, one / two / four pieces a lane / ring:
-//   148 rows 2.5 / 2.9 / 3.6 / 4.4   600 rows 4.8 / 3.8 / 4.5 / 5.0
-//   1,000 rows 6.5 / 5.7 / 4.7 / 5.6   16,384 rows - / - / 52.0 / 47.1
-// and at d = 1,024: 1,000 rows 2.9 / 3.0 / 3.7, 6,144 rows - / - / 7.3 / 6.8.
-// With the checkpoint written too the ring is not faster (67.2 against 65.4 at
-// 16,384 x 4,096) and is not built.
-constexpr int64_t kOnePiece = 148 * 1024, kTwoPieces = 148 * 2560, kRingPieces = 148 * 4608;
 template <int kN>
 constexpr int bwd_stages() { return kN == 1 ? 10 : 6; }
 
@@ -1023,6 +1025,17 @@ static dlm_status_t launch_fwd(void (*kern)(NormFwdArgs), const NormFwdArgs& a, 
     return launch_pdl(kern, dim3(unsigned((a.rows + kG - 1) / kG)), dim3(kNW * kG * 32), 0, s, "k_norm_fwd launch", a);
 }
 
+// Which forward kernel, by the call's 16-byte pieces (rows x d / 8).  The fewer,
+// the more warps share a row, so that one row's time, not the bandwidth,
+// counts less; the ring pays once its start is spread over enough rows.
+// Measured (us), d = 4,096, one / two / four pieces a lane / ring:
+//   148 rows 2.5 / 2.9 / 3.6 / 4.4   600 rows 4.8 / 3.8 / 4.5 / 5.0
+//   1,000 rows 6.5 / 5.7 / 4.7 / 5.6   16,384 rows - / - / 52.0 / 47.1
+// and at d = 1,024: 1,000 rows 2.9 / 3.0 / 3.7, 6,144 rows - / - / 7.3 / 6.8.
+// With the checkpoint written too the ring is not faster (67.2 against 65.4 at
+// 16,384 x 4,096) and is not built.
+constexpr int64_t kOnePiece = 148 * 1024, kTwoPieces = 148 * 2560, kRingPieces = 148 * 4608;
+
 // warps that a row of `pieces` pieces takes at `per` pieces a lane: a power of
 // two up to 32, 0 if they do not hold it
 static int warps_for(int64_t pieces, int per) {
@@ -1116,7 +1129,8 @@ static dlm_status_t launch_any(const Args& a, RingShape sh, int tensors, cudaStr
 // The backward pass leaves one partial row per CTA, of which there is at most
 // one per SM, whatever the kernel.
 // Up to so many rows a group, one CTA takes them all and writes the gradients
-// itself: its rows, one after the other, take no longer than a second launch.
+// itself, without a second launch (d = 4,096, GPU time alone: 2 rows 5.9 us in
+// one launch, 5 rows 6.4 in two; 4 rows a group took 9.0 against 6.4).
 constexpr int kAloneRows = 2;
 
 struct NormBwdPlan { unsigned grid; int pitch; size_t bytes; };
