@@ -591,7 +591,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     uint16_t* pdx = a.dx + first * a.ld_dx + t * 8 - phase;
     int par = 0;
     for (; n > 0; --n, par ^= 1, pdx += step * a.ld_dx) {
-        const uint64_t nm = f2splat(-mean_n), r2 = f2splat(rstd_n);
+        const float rstd = rstd_n;
+        const uint64_t nm = f2splat(-mean_n), r2 = f2splat(rstd);
         float qs[kN], qs2[kN];
         if constexpr (kHeld8) {
             #pragma unroll
@@ -648,12 +649,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
         f2unpack(s2, lo, hi);
         v2 = lo + hi;
         group_sum2(v1, v2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
-        const uint64_t n1 = f2splat(a.rms ? 0.f : -v1 * inv_d), n2 = f2splat(-v2 * inv_d);
+        const float by = -rstd * inv_d;
+        const uint64_t n1 = f2splat(a.rms ? 0.f : v1 * by), n2 = f2splat(v2 * by);
         #pragma unroll
         for (int j = 0; j < kN; ++j) {
             uint64_t o[4];
             #pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = f2mul(f2add(f2fma(xh[j][k], n2, gr[j][k]), n1), r2);
+            for (int k = 0; k < 4; ++k) o[k] = f2fma(gr[j][k], r2, f2fma(xh[j][k], n2, n1));
             pc.store(j, a.d, pdx + j * gt * 8, o);
         }
     }
