@@ -417,11 +417,14 @@ class LinearOut:
 def _aligned_workspace(nbytes: int, device, align: int = 1024) -> torch.Tensor:
     """A uint8 workspace whose first byte is `align`-byte aligned (the loss
     needs 256, the fused head 1024; the caching allocator guarantees 512 and
-    other allocators less): where it is not, a slice of a slightly larger
-    buffer, which the slice keeps alive."""
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if buf.data_ptr() % align == 0:
-        return buf
+    other allocators less): where that is not so by itself, a slice of a
+    slightly larger buffer, which the slice keeps alive.  (Two buffers are never
+    held at once, and one as large as the fused head's is asked for once.)"""
+    if align <= 512:
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if buf.data_ptr() % align == 0:
+            return buf
+        del buf
     buf = torch.empty(nbytes + align - 1, dtype=torch.uint8, device=device)
     off = (-buf.data_ptr()) % align
     return buf[off:off + nbytes]

@@ -676,7 +676,7 @@ struct EmbPlan {
 };
 
 static bool embed_plan(const dlm_layout_t* L, int32_t vocab, int32_t d, EmbPlan* p) {
-    if (!layout_ok(L) || vocab < 1 || d < 1 || vocab == INT32_MAX || d > INT32_MAX - 64) return false;
+    if (!layout_ok(L) || vocab < 1 || d < 1 || vocab == INT32_MAX || d > INT32_MAX - 1024) return false;
     p->chunk = kMaxChunk;
     while (p->chunk > kMinChunk && L->n_tokens / p->chunk * ((int64_t(d) + 255) / 256) < 148 * 16) p->chunk /= 2;
     p->chunks = (L->n_tokens + p->chunk - 1) / p->chunk;

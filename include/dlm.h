@@ -63,6 +63,8 @@
  *     word; the affected rows are treated as unscored and the call still
  *     completes.  Read the word with dlm_get_device_status.
  *   - bf16 tensors are passed as uint16_t bit patterns (IEEE bfloat16).
+ *   - Pointers lie on borders of their element type (2 bytes for bf16, 4 for
+ *     float and int32), also where a void pointer stands for either.
  *   - Outputs do not overlap inputs or each other (dlm_scale_bf16 and the
  *     accumulate options, which update a buffer, apart).
  *   - Requires compute capability 10.0 (B200); other devices get
@@ -534,8 +536,8 @@ DLM_API dlm_status_t dlm_scale_bf16(uint16_t *x, int64_t rows, int64_t cols, int
  * Errors: a bad layout, vocab or d_model < 1, a row stride < d_model, a scale
  * that is not finite or a null pointer return DLM_ERR_INVALID_ARGUMENT.
  * n_tokens = 0 is a no-op.  Rows on 16-byte borders (d_model and strides
- * multiples of 8, aligned pointers) take 16-byte accesses, others single
- * elements, with the same results.
+ * multiples of 8, aligned pointers) are accessed as they lie, others by the
+ * 16-byte chunks that cover them, with the same results.
  * The pages have no counterpart: they train whole models, whose input this
  * is.
  * ---------------------------------------------------------------------- */

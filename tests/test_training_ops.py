@@ -4,6 +4,7 @@ turned into status codes, and the 64-bit forms that the GPU tests compare with,
 themselves held to central differences and to the 8-bit format's own
 definition."""
 import ctypes
+import weakref
 
 import pytest
 import torch
@@ -377,3 +378,36 @@ def test_bounds_refuse_planted_mistakes():
     ref.assert_within(de.to(bf16), de, be)
     refused(ref.embed_grad(ids[1:], dy[1:], 9, 2.0)[0].to(bf16), de, be)
     refused(ref.embed_grad(ids, dy, 9, 4.0)[0].to(bf16), de, be)
+
+
+def test_no_second_workspace_is_asked_for_while_one_is_held(monkeypatch):
+    """The buffers are several GB for the fused head: one request for it, and
+    for the others never two buffers alive at once, whatever the allocator
+    returns."""
+    empty, alive, asked, most = torch.empty, [], [], []
+
+    def off_border(n, **kw):
+        buf = empty(n + 8192, **kw)
+        at = (-buf.data_ptr()) % 4096 + 16           # on a 16-byte border only
+        buf = buf[at:at + n]
+        alive.append(weakref.ref(buf))
+        asked.append(n)
+        most.append(sum(r() is not None for r in alive[:-1]))
+        return buf
+    monkeypatch.setattr(torch, "empty", off_border)
+    for align, requests in ((1024, 1), (256, 2)):
+        alive.clear(), asked.clear(), most.clear()
+        ws = dlm._aligned_workspace(5000, "cpu", align)
+        assert ws.numel() == 5000 and ws.data_ptr() % align == 0
+        assert len(asked) == requests and max(most) == 0
+
+
+def test_widths_that_would_pass_32_bits_are_refused(L):
+    """Both passes count columns in 32 bits, in steps of up to 1,024."""
+    lay = dlm.Layout(1, 4, 4, None, None)
+    p = ctypes.byref(lay)
+    for d in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 1024):
+        assert L.dlm_embed_fwd(p, 16, 16, d, 4, d, 1.0, 16, d, None, None) == INVALID
+        assert L.dlm_embed_bwd_workspace_size(p, d, 4) == 0
+        assert L.dlm_embed_bwd(p, 16, 16, d, 4, d, 1.0, 0, 0, 16, d, 256, 2 ** 62, None) == INVALID
+        assert L.dlm_norm_bwd_workspace_size(4, d) == 0
