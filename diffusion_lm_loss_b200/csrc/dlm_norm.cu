@@ -11,7 +11,7 @@
 // should be bound by HBM.  What has to be kept small beside that is the
 // instructions per element (packed fp32 pairs, parameters in registers) and
 // the exchanges per row.  Measured at 16,384 x 4,096 with weight and bias:
-// forward 47 us (0.87 of the copy rate; one warp group per row without a ring
+// forward 46 us (0.89 of the copy rate; one warp group per row without a ring
 // 52, per row of one warp 105), backward 71 us (0.86; one row per CTA of 16
 // warps with plain loads 194), forward that also writes the checkpoint 65 us
 // (0.79, issue-bound: the codes double the instructions), backward from it 76
@@ -243,7 +243,10 @@ struct RingShape { int nw, groups; };
 
 // The sums of s1 and s2 over a group, in every lane.  Lanes 0..15 carry s1,
 // 16..31 s2.  slot: [nw] float2 that no earlier exchange still reads; `bar`:
-// the group's barrier.
+// the group's barrier.  kAdd: every lane adds up to 8 warps' sums itself in
+// place of four more shuffles (forward, 16,384 x 4,096: 47.4 -> 46.1 us; the
+// backward pass, short of registers, gets slower: 70.5 -> 72.0).
+template <bool kAdd>
 __device__ __forceinline__ void group_sum2(float& s1, float& s2, float2* slot, int wg, const RingShape sh, int bar) {
     const int lane = threadIdx.x & 31;
     float v = lane < 16 ? s1 : s2;
@@ -253,6 +256,17 @@ __device__ __forceinline__ void group_sum2(float& s1, float& s2, float2* slot, i
     if (sh.nw > 1) {
         if ((lane & 15) == 0) reinterpret_cast<float*>(slot + wg)[lane >> 4] = v;
         named_barrier_sync(bar, sh.nw * 32);
+        if (kAdd && sh.nw <= 8) {
+            uint64_t p[8];
+            #pragma unroll
+            for (int w = 0; w < 8; ++w) p[w] = w < sh.nw ? *reinterpret_cast<const uint64_t*>(slot + w) : 0;
+            #pragma unroll
+            for (int o = 4; o; o >>= 1)
+                #pragma unroll
+                for (int w = 0; w < o; ++w) p[w] = f2add(p[w], p[w + o]);
+            f2unpack(p[0], s1, s2);
+            return;
+        }
         v = (lane & 15) < sh.nw ? reinterpret_cast<const float*>(slot + (lane & 15))[lane >> 4] : 0.f;
         #pragma unroll
         for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
@@ -463,7 +477,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
         ring.step(ring.get);
         issue();
         if (a.rms) s1[0] = s1[1] = 0.f;
-        else group_sum2(s1[0], s1[1], &s_x[par][0][g * sh.nw], wg, sh, 1 + g);
+        else group_sum2<!kShift>(s1[0], s1[1], &s_x[par][0][g * sh.nw], wg, sh, 1 + g);
         #pragma unroll
         for (int r = 0; r < kR; ++r) {
             s1[r] *= inv_d;                               // the mean
@@ -480,7 +494,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
             f2unpack(sq, lo, hi);
             s2[r] = lo + hi;
         }
-        group_sum2(s2[0], s2[1], &s_x[par][1][g * sh.nw], wg, sh, 1 + g);
+        group_sum2<!kShift>(s2[0], s2[1], &s_x[par][1][g * sh.nw], wg, sh, 1 + g);
         #pragma unroll
         for (int r = 0; r < kR; ++r) {
             if (n <= r) break;
@@ -648,7 +662,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
         v1 = lo + hi;
         f2unpack(s2, lo, hi);
         v2 = lo + hi;
-        group_sum2(v1, v2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
+        group_sum2<false>(v1, v2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
         const float by = -rstd * inv_d;
         const uint64_t n1 = f2splat(a.rms ? 0.f : v1 * by), n2 = f2splat(v2 * by);
         #pragma unroll
@@ -863,7 +877,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_any(NormBwdArgs a,
             dw[k] += dy[k] * xh[k];
             db[k] += dy[k];
         }
-        group_sum2(s1, s2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
+        group_sum2<false>(s1, s2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
         const float m1 = a.rms ? 0.f : s1 * inv_d, m2 = s2 * inv_d;
         uint16_t* dx = a.dx + row * a.ld_dx;
         #pragma unroll
@@ -1032,7 +1046,7 @@ static dlm_status_t launch_fwd(void (*kern)(NormFwdArgs), const NormFwdArgs& a, 
 // counts less; the ring pays once its start is spread over enough rows.
 // Measured (us), d = 4,096, one / two / four pieces a lane / ring:
 //   148 rows 2.5 / 2.9 / 3.6 / 4.4   600 rows 4.8 / 3.8 / 4.5 / 5.0
-//   1,000 rows 6.5 / 5.7 / 4.7 / 5.6   16,384 rows - / - / 52.0 / 47.1
+//   1,000 rows 6.5 / 5.7 / 4.7 / 5.6   16,384 rows - / - / 52.0 / 46.2
 // and at d = 1,024: 1,000 rows 2.9 / 3.0 / 3.7, 6,144 rows - / - / 7.3 / 6.8.
 // With the checkpoint written too the ring is not faster (67.2 against 65.4 at
 // 16,384 x 4,096) and is not built.
