@@ -160,6 +160,38 @@ def test_gradient_pads_strides_and_accumulate(t, vocab, d, ld, ldw, shift, dtype
     assert bool((rest == 7.0).all()), "wrote outside its columns"
 
 
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("d", [264, 1001])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_rows_over_few_and_many_chunks(d, dtype, accumulate):
+    """Tokens drawn as words are, and rows of just under, just as many and just
+    more tokens than 1 to 20 chunks of 8, 16 and 32 hold, side by side."""
+    g = _gen(d)
+    vocab = 400
+    p = 1.0 / torch.arange(1, vocab + 1, device="cuda")
+    words = torch.multinomial(p / p.sum(), 3000, replacement=True, generator=g).int()
+    runs = [c * n + e for c in (8, 16, 32) for n in (1, 2, 7, 8, 9, 10, 17, 20) for e in (-1, 0, 1)]
+    rows = torch.repeat_interleave(torch.arange(len(runs), device="cuda"), torch.tensor(runs, device="cuda")).int()
+    for ids in (words, rows[torch.randperm(rows.numel(), generator=g, device="cuda")]):
+        dy = _randn((ids.numel(), d), g)
+        lay = dlm.make_layout(1, ids.numel())
+        dw, mag = ref.embed_grad(ids, dy, vocab, 3.0)
+        old = _randn((vocab, d), g, dtype) if accumulate else torch.full((vocab, d), float("nan"), dtype=dtype, device="cuda")
+        got = old.clone()
+        dlm.embed_bwd(lay, ids, dy, vocab, 3.0, d_weight=got, accumulate=accumulate)
+        if accumulate:
+            untouched = mag.abs().sum(1) == 0
+            assert torch.equal(got[untouched], old[untouched])
+            dw, mag = old.double() + dw, mag + old.double().abs()
+            bound = ref.embed_grad_bound(ids, dw, mag, dtype)
+            ref.assert_within(got[~untouched], dw[~untouched], bound[~untouched])
+        else:
+            ref.assert_within(got, dw, ref.embed_grad_bound(ids, dw, mag, dtype))
+        again = old.clone()
+        dlm.embed_bwd(lay, ids, dy, vocab, 3.0, d_weight=again, accumulate=accumulate)
+        assert torch.equal(again, got)
+
+
 def test_gradient_no_tokens_all_pads_bad_ids():
     g = _gen(3)
     dy = _randn((6, 64), g)
