@@ -100,17 +100,18 @@ struct EmbHeader {
     uint32_t status;      // DLM_DEV_* bits of this call
 };
 
-// Calls f(token, id, valid) for the tokens of one warp's section, 128 at a
-// time with kDeep times as many loaded ahead; every lane takes part in every
-// call.
+// Calls f(token, ids) for the tokens of one warp's section, 128 at a time, four
+// consecutive ones a lane, with kDeep times as many loaded ahead; every lane
+// takes part in every call.  Pads and places without a token come as id -1.
+// bad: becomes true where a token that is no pad has an id outside [0, vocab);
+// NULL: not looked for.
 template <int kDeep, typename F>
 __device__ __forceinline__ void for_section(const int32_t* __restrict__ ids, const uint8_t* __restrict__ pad,
-                                            int64_t beg, int64_t end, bool wide, F&& f) {
+                                            int64_t beg, int64_t end, bool wide, int vocab, bool* bad, F&& f) {
     const int lane = threadIdx.x & 31;
     #pragma unroll 1
     for (int64_t i = beg; i < end; i += 128 * kDeep) {
         int id[kDeep][4];
-        uint32_t out = 0;                  // bit 4 k + e: no token, or a pad
         #pragma unroll
         for (int k = 0; k < kDeep; ++k) {
             const int64_t at = i + 128 * k + lane * 4;
@@ -119,19 +120,68 @@ __device__ __forceinline__ void for_section(const int32_t* __restrict__ ids, con
                 id[k][0] = q.x; id[k][1] = q.y; id[k][2] = q.z; id[k][3] = q.w;
             } else {
                 #pragma unroll
-                for (int e = 0; e < 4; ++e) id[k][e] = at + e < end ? __ldg(ids + at + e) : 0;
+                for (int e = 0; e < 4; ++e) id[k][e] = at + e < end ? __ldg(ids + at + e) : -1;
             }
+        }
+        uint32_t pads = 0;                 // bit 4 k + e: a pad, or no token
+        if (pad || i + 128 * kDeep > end) {
             #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (at + e >= end || (pad && pad[at + e])) out |= 1u << (4 * k + e);
+            for (int k = 0; k < kDeep; ++k)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t at = i + 128 * k + lane * 4 + e;
+                    if (at >= end || (pad && pad[at])) pads |= 1u << (4 * k + e);
+                }
+        }
+        if (bad) {
+            #pragma unroll
+            for (int k = 0; k < kDeep; ++k)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (uint32_t(id[k][e]) >= uint32_t(vocab) && !(pads >> (4 * k + e) & 1)) *bad = true;
         }
         #pragma unroll
         for (int k = 0; k < kDeep; ++k) {
             if (i + 128 * k >= end) break;
             #pragma unroll
             for (int e = 0; e < 4; ++e)
-                f(int(i + 128 * k + lane * 4 + e), id[k][e], !(out >> (4 * k + e) & 1));
+                if (pads >> (4 * k + e) & 1) id[k][e] = -1;
+            f(int(i + 128 * k) + lane * 4, id[k]);
         }
+    }
+}
+
+// How many of a section's tokens each of the rows v0 .. v0 + n - 1 has: added to
+// mine, which is this warp's.
+__device__ __forceinline__ void count_rows(const int (&id)[4], int v0, int n, int* mine) {
+    #pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (uint32_t(id[e]) - uint32_t(v0) < uint32_t(n)) atomicAdd(&mine[id[e] - v0], 1);
+}
+
+// Calls put(place, token, row) for the tokens of these rows; mine: each row's
+// next place, advanced.  The order within 128 tokens is that of (token mod 4, token).
+template <typename Put>
+__device__ __forceinline__ void place_rows(int token, const int (&id)[4], int v0, int n, int* mine, Put&& put) {
+    const int lane = threadIdx.x & 31;
+    bool any = false;
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) any |= uint32_t(id[e]) - uint32_t(v0) < uint32_t(n);
+    if (!__ballot_sync(~0u, any)) return;
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int r = int(uint32_t(id[e]) - uint32_t(v0));
+        const bool in = uint32_t(r) < uint32_t(n);
+        const uint32_t m = __ballot_sync(~0u, in);
+        if (m == 0) continue;
+        if (in) {
+            const uint32_t peers = __match_any_sync(m, r);
+            const int first = mine[r], rank = __popc(peers & ((1u << lane) - 1u));
+            put(first + rank, token + e, r);
+            __syncwarp(m);
+            if (rank == 0) mine[r] = first + __popc(peers);
+        }
+        __syncwarp();
     }
 }
 
@@ -158,18 +208,10 @@ __global__ void __launch_bounds__(1024) k_embed_sort(const int32_t* __restrict__
 
     int below = 0;
     bool bad = false;
-    for_section<4>(ids, pad, beg, end, wide, [&](int, int id, bool valid) {
-        bad |= valid && uint32_t(id) >= uint32_t(vocab);
-        below += valid && id >= 0 && id < v0;
-        const int r = id - v0;
-        const bool in = valid && uint32_t(r) < uint32_t(n);
-        const uint32_t m = __ballot_sync(~0u, in);
-        if (m == 0) return;
-        if (in) {
-            const uint32_t peers = __match_any_sync(m, r);
-            if (lane == __ffs(peers) - 1) mine[r] += __popc(peers);
-        }
-        __syncwarp();
+    for_section<4>(ids, pad, beg, end, wide, vocab, blockIdx.x == 0 ? &bad : nullptr, [&](int, const int (&id)[4]) {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) below += uint32_t(id[e]) < uint32_t(v0);
+        count_rows(id, v0, n, mine);
     });
     below = __reduce_add_sync(~0u, below);
     if (lane == 0 && below) atomicAdd(&s_below, below);
@@ -209,21 +251,11 @@ __global__ void __launch_bounds__(1024) k_embed_sort(const int32_t* __restrict__
         __syncthreads();
     }
 
-    for_section<4>(ids, pad, beg, end, wide, [&](int i, int id, bool valid) {
-        const int r = id - v0;
-        const bool in = valid && uint32_t(r) < uint32_t(n);
-        const uint32_t m = __ballot_sync(~0u, in);
-        if (m == 0) return;
-        if (in) {
-            const uint32_t peers = __match_any_sync(m, r);
-            const int first = mine[r];
-            const int rank = __popc(peers & ((1u << lane) - 1u));
-            order[first + rank] = i;
-            sid[first + rank] = id;
-            __syncwarp(m);
-            if (rank == 0) mine[r] = first + __popc(peers);
-        }
-        __syncwarp();
+    for_section<4>(ids, pad, beg, end, wide, vocab, nullptr, [&](int token, const int (&id)[4]) {
+        place_rows(token, id, v0, n, mine, [&](int at, int i, int r) {
+            order[at] = i;
+            sid[at] = v0 + r;
+        });
     });
 }
 
@@ -588,19 +620,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32) k_embed_small(EmbSmallArgs a
     const int beg = min(a.n_tokens, warp * per), end = min(a.n_tokens, beg + per);
     int* mine = s_place[warp];
     bool bad = false, any = false;
-    for_section<1>(a.ids, a.pad, beg, end, a.wide, [&](int, int id, bool valid) {
-        bad |= valid && uint32_t(id) >= uint32_t(a.vocab);
-        const int r = id - v0;
-        const bool in = valid && uint32_t(r) < uint32_t(n);
-        const uint32_t m = __ballot_sync(~0u, in);
-        if (m == 0) return;
-        any = true;
-        if (in) {
-            const uint32_t peers = __match_any_sync(m, r);
-            if (lane == __ffs(peers) - 1) mine[r] += __popc(peers);
-        }
-        __syncwarp();
+    for_section<1>(a.ids, a.pad, beg, end, a.wide, a.vocab, blockIdx.x == 0 ? &bad : nullptr,
+                   [&](int, const int (&id)[4]) {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) any |= uint32_t(id[e]) - uint32_t(v0) < uint32_t(n);
+        count_rows(id, v0, n, mine);
     });
+    any = __any_sync(~0u, any);
     if (blockIdx.x == 0) {
         bad = __syncthreads_or(bad);
         if (threadIdx.x == 0) a.hdr->status = bad ? DLM_DEV_BAD_TOKEN_ID : 0u;
@@ -627,20 +653,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32) k_embed_small(EmbSmallArgs a
     }
     __syncthreads();
     if (any)
-        for_section<1>(a.ids, a.pad, beg, end, a.wide, [&](int i, int id, bool valid) {
-            const int r = id - v0;
-            const bool in = valid && uint32_t(r) < uint32_t(n);
-            const uint32_t m = __ballot_sync(~0u, in);
-            if (m == 0) return;
-            if (in) {
-                const uint32_t peers = __match_any_sync(m, r);
-                const int first = mine[r], rank = __popc(peers & ((1u << lane) - 1u));
-                s_tok[first + rank] = uint16_t(i);
-                s_row[first + rank] = int8_t(r);
-                __syncwarp(m);
-                if (rank == 0) mine[r] = first + __popc(peers);
-            }
-            __syncwarp();
+        for_section<1>(a.ids, a.pad, beg, end, a.wide, a.vocab, nullptr, [&](int token, const int (&id)[4]) {
+            place_rows(token, id, v0, n, mine, [&](int at, int i, int r) {
+                s_tok[at] = uint16_t(i);
+                s_row[at] = int8_t(r);
+            });
         });
     __syncthreads();
     const int count = s_count, part = (count + kSmallWarps - 1) / kSmallWarps;
