@@ -269,23 +269,41 @@ __device__ __forceinline__ void put_grad_value(uint16_t* dst, float v) {
     *dst = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// What 8 elements of a gradient on a 16-byte border held (zeros where it is not
+// added to), and the same with scale * acc added, stored.
+template <typename GT> constexpr int kOldWords = sizeof(GT) / 2;      // of 16 bytes
+template <typename GT>
+__device__ __forceinline__ void load_old(const GT* src, bool there, uint4 (&old)[kOldWords<GT>]) {
+    #pragma unroll
+    for (int h = 0; h < kOldWords<GT>; ++h) {
+        old[h] = make_uint4(0, 0, 0, 0);
+        if (there)
+            asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(old[h].x), "=r"(old[h].y), "=r"(old[h].z), "=r"(old[h].w)
+                         : "l"(reinterpret_cast<const uint4*>(src) + h) : "memory");
+    }
+}
+__device__ __forceinline__ void put8(float* dst, const float (&acc)[8], float scale, const uint4 (&old)[2]) {
+    #pragma unroll
+    for (int h = 0; h < 2; ++h)
+        reinterpret_cast<float4*>(dst)[h] =
+            make_float4(__uint_as_float(old[h].x) + scale * acc[4 * h], __uint_as_float(old[h].y) + scale * acc[4 * h + 1],
+                        __uint_as_float(old[h].z) + scale * acc[4 * h + 2], __uint_as_float(old[h].w) + scale * acc[4 * h + 3]);
+}
+__device__ __forceinline__ void put8(uint16_t* dst, const float (&acc)[8], float scale, const uint4 (&old)[1]) {
+    uint32_t x[4] = {old[0].x, old[0].y, old[0].z, old[0].w};
+    #pragma unroll
+    for (int k = 0; k < 4; ++k)
+        x[k] = pack_bf16x2(bf16lo(x[k]) + scale * acc[2 * k], bf16hi(x[k]) + scale * acc[2 * k + 1]);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 template <int kVec, typename GT>
 __device__ __forceinline__ void put_row(GT* __restrict__ dst, const float (&acc)[kVec], float scale, bool accumulate) {
-    if constexpr (kVec == 8 && std::is_same<GT, float>::value) {
-        #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float4 o = accumulate ? reinterpret_cast<const float4*>(dst)[h] : make_float4(0.f, 0.f, 0.f, 0.f);
-            o.x += scale * acc[4 * h]; o.y += scale * acc[4 * h + 1];
-            o.z += scale * acc[4 * h + 2]; o.w += scale * acc[4 * h + 3];
-            reinterpret_cast<float4*>(dst)[h] = o;
-        }
-    } else if constexpr (kVec == 8) {
-        const uint4 o = accumulate ? *reinterpret_cast<const uint4*>(dst) : make_uint4(0, 0, 0, 0);
-        uint32_t x[4] = {o.x, o.y, o.z, o.w};
-        #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            x[k] = pack_bf16x2(bf16lo(x[k]) + scale * acc[2 * k], bf16hi(x[k]) + scale * acc[2 * k + 1]);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+    if constexpr (kVec == 8) {
+        uint4 old[kOldWords<GT>];
+        load_old(dst, accumulate, old);
+        put8(dst, acc, scale, old);
     } else {
         put_grad_value(dst, (accumulate ? grad_value(*dst) : 0.f) + scale * acc[0]);
     }
@@ -375,9 +393,11 @@ __device__ __forceinline__ void zero_rows(const EmbGradArgs& a, int64_t cta, int
 // kAligned: rows of d_out and d_weight on 16-byte borders.  Otherwise d_out is
 // read as dlm_shift.cuh does, and a finished row is written by single elements
 // side by side, through a warp's 1 KB of shared memory.
-template <bool kAligned, typename GT>
+// kAdd: added to what d_weight holds, which is read ahead with the rows
+// (16,384 x 4,096: READAHEAD).
+template <bool kAligned, bool kAdd, typename GT>
 __global__ void __launch_bounds__(kGradThreads) k_embed_grad(EmbGradArgs a) {
-    constexpr int kU = kAligned ? 8 : 4;       // rows in flight
+    constexpr int kU = kAligned && !kAdd ? 8 : 4;       // rows in flight
     extern __shared__ float s_rows[];          // not kAligned: [warp][256]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
@@ -407,12 +427,18 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(EmbGradArgs a) {
     const uint16_t* end = a.d_out + (a.n_tokens - 1) * a.ld + a.d;
     for (int p = 0; p < n; p += kU) {
         uint4 q[kU], more[kU];                 // more: the chunk behind the last lane's
+        uint4 old[kAligned && kAdd ? kU : 1][kOldWords<GT>];
         int sh[kU];
         #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const uint16_t* at = column + __shfl_sync(~0u, tok, min(p + u, n - 1)) * a.ld;
             if constexpr (kAligned) {
                 q[u] = load_piece<8>(at);
+                if constexpr (kAdd) {          // a row that ends here and is written by this thread
+                    const int id = __shfl_sync(~0u, row, (p + u) & 31), nx = __shfl_sync(~0u, row, (p + u + 1) & 31);
+                    const bool ends = p + u < n && id != (p + u + 1 == n ? after : nx) && id != before;
+                    load_old(dw + int64_t(ends ? id : 0) * a.ld_dw + col, ends && active, old[u]);
+                }
             } else {
                 sh[u] = int(reinterpret_cast<uintptr_t>(at) & 15) / 2;
                 q[u] = col - sh[u] < a.d ? load_chunk(at - sh[u], a.d_out, end) : make_uint4(0, 0, 0, 0);
@@ -439,18 +465,27 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(EmbGradArgs a) {
                     for (int k = 0; k < 8; ++k)
                         if (kAligned ? active : col + k < a.d) dst[k] = acc[k];
                 } else if constexpr (kAligned) {
-                    if (active) put_row<8, GT>(dw + int64_t(id) * a.ld_dw + col, acc, a.scale, a.accumulate);
+                    GT* dst = dw + int64_t(id) * a.ld_dw + col;
+                    if constexpr (kAdd) {
+                        if (active) put8(dst, acc, a.scale, old[u]);
+                    } else {
+                        if (active) put_row<8, GT>(dst, acc, a.scale, false);
+                    }
                 } else {
                     __syncwarp();
                     #pragma unroll
                     for (int k = 0; k < 8; ++k) s_rows[warp * 256 + lane * 8 + k] = acc[k];
                     __syncwarp();
+                    GT* dst = dw + int64_t(id) * a.ld_dw + col - lane * 8;
+                    const int left = a.d - (col - lane * 8);
+                    float o[8];
                     #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int at = lane + 32 * k, cc = col - lane * 8 + at;
-                        const float v[1] = {s_rows[warp * 256 + at]};
-                        if (cc < a.d) put_row<1, GT>(dw + int64_t(id) * a.ld_dw + cc, v, a.scale, a.accumulate);
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = kAdd && lane + 32 * k < left ? grad_value(dst[lane + 32 * k]) : 0.f;
+                    #pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (lane + 32 * k < left)
+                            put_grad_value(dst + lane + 32 * k, o[k] + a.scale * s_rows[warp * 256 + lane + 32 * k]);
                 }
                 open = false;
                 #pragma unroll
@@ -834,8 +869,10 @@ extern "C" dlm_status_t dlm_embed_bwd(const dlm_layout_t* layout, const int32_t*
     a.pitch = p.pitch; a.chunk = p.chunk; a.tiles = tiles; a.n_tokens = layout->n_tokens; a.chunk_ctas = p.chunks * tiles;
     a.join_ctas = join_ctas; a.join_tiles = join_tiles; a.zero_rows = zero_rows; a.zero_split = zero_split;
     if (a.chunk_ctas + zero_grad > 0) {
-        auto kern = f32 ? (vec ? k_embed_grad<true, float> : k_embed_grad<false, float>)
-                        : (vec ? k_embed_grad<true, uint16_t> : k_embed_grad<false, uint16_t>);
+        auto kern = f32 ? (vec ? (accumulate ? k_embed_grad<true, true, float> : k_embed_grad<true, false, float>)
+                               : (accumulate ? k_embed_grad<false, true, float> : k_embed_grad<false, false, float>))
+                        : (vec ? (accumulate ? k_embed_grad<true, true, uint16_t> : k_embed_grad<true, false, uint16_t>)
+                               : (accumulate ? k_embed_grad<false, true, uint16_t> : k_embed_grad<false, false, uint16_t>));
         st = launch_pdl(kern, dim3(unsigned(a.chunk_ctas + zero_grad)), dim3(threads), vec ? 0 : threads * 8 * sizeof(float),
                         s, "k_embed_grad launch", a);
         if (st != DLM_OK) return st;
