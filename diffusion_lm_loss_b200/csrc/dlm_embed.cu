@@ -22,8 +22,10 @@
 // The rows that no token has are written by more CTAs of the last two launches.
 // Nothing is added atomically: results are bitwise reproducible.  The table's
 // gradient has to be written once and every token's row read once: 16,384
-// tokens, half of them masked, on a table of 1 GB take 188 us, 0.95 of the copy
-// rate; about 12 us of that is the sort, which nothing hides.
+// tokens, half of them masked, on a table of 1 GB take 184 us, 0.97 of the copy
+// rate; about 8 us of that is the sort, which nothing hides (zeroing part of the
+// table beside it gained nothing: the memory is still writing what came before).
+// Added to another gradient they take 60 us, 0.67.
 #include <type_traits>
 
 #include "dlm_device.cuh"
@@ -394,7 +396,8 @@ __device__ __forceinline__ void zero_rows(const EmbGradArgs& a, int64_t cta, int
 // read as dlm_shift.cuh does, and a finished row is written by single elements
 // side by side, through a warp's 1 KB of shared memory.
 // kAdd: added to what d_weight holds, which is read ahead with the rows
-// (16,384 x 4,096: READAHEAD).
+// (16,384 x 4,096, half of them masked: 65 -> 60 us; with 8 rows in flight
+// instead of 4, on 112 registers instead of 72, again 65).
 template <bool kAligned, bool kAdd, typename GT>
 __global__ void __launch_bounds__(kGradThreads) k_embed_grad(EmbGradArgs a) {
     constexpr int kU = kAligned && !kAdd ? 8 : 4;       // rows in flight
