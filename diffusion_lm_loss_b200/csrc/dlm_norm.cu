@@ -302,9 +302,10 @@ __device__ __forceinline__ void param_pairs(const void* p, int f32, int c, float
     for (int k = 0; k < 4; ++k) o[k] = f2pack(v[2 * k] + add, v[2 * k + 1] + add);
 }
 
-// Stages of the rings: with one or two pieces a lane 80 or 160 KB (forward), 164
-// or 197 KB (backward) of shared memory, all but one stage of it in flight.
-constexpr int kFwdStages = 5;
+// Stages of the rings, with kN pieces a lane: 80 to 196 KB (forward), 164 or 197
+// KB (backward) of shared memory, all but one stage of it in flight.
+template <int kN>
+constexpr int fwd_stages() { return kN == 3 ? 4 : 5; }
 template <int kN>
 constexpr int bwd_stages() { return kN == 1 ? 10 : 6; }
 
@@ -405,7 +406,7 @@ struct Pieces {
 
 template <int kN, bool kShift>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a, RingShape sh) {
-    constexpr int kS = kFwdStages, kR = 2;                // two rows at a time: their exchanges share barriers
+    constexpr int kS = fwd_stages<kN>(), kR = 2;                // two rows at a time: their exchanges share barriers
     extern __shared__ uint4 ring_mem[];
     __shared__ float2 s_x[2][2][kRingThreads / 32];       // [turn parity][sum][warp]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1053,32 +1054,51 @@ static dlm_status_t launch_fwd(void (*kern)(NormFwdArgs), const NormFwdArgs& a, 
 constexpr int64_t kOnePiece = 148 * 1024, kTwoPieces = 148 * 2560, kRingPieces = 148 * 4608;
 
 // warps that a row of `pieces` pieces takes at `per` pieces a lane: a power of
-// two up to 32, 0 if they do not hold it
+// two up to 32, with four a lane any number up to 8; 0 if they do not hold it.
+// (With the checkpoint, 13,107 x 5,120: 91.1 us with 8 warps, 69.0 with 5.)
 static int warps_for(int64_t pieces, int per) {
-    for (int nw = 1; nw <= 32; nw *= 2)
+    for (int nw = 1; nw <= 32; nw = per == 4 && nw < 8 ? nw + 1 : 2 * nw)
         if (pieces <= int64_t(nw) * 32 * per) return nw;
     return 0;
 }
 
 template <int kN>
-static dlm_status_t launch_fwd_vec(int nw, const NormFwdArgs& a, cudaStream_t s) {
-    switch (nw) {
+static dlm_status_t launch_fwd_vec(const NormFwdArgs& a, cudaStream_t s) {
+    switch (warps_for(a.d / 8, kN)) {
         case 1: return launch_fwd<1>(k_norm_fwd_vec<kN, 1>, a, s);
         case 2: return launch_fwd<2>(k_norm_fwd_vec<kN, 2>, a, s);
         case 4: return launch_fwd<4>(k_norm_fwd_vec<kN, 4>, a, s);
         case 8: return launch_fwd<8>(k_norm_fwd_vec<kN, 8>, a, s);
         case 16: return launch_fwd<16>(k_norm_fwd_vec<kN, 16>, a, s);
-        default: return launch_fwd<32>(k_norm_fwd_vec<kN, 32>, a, s);
+        default: break;
     }
+    if constexpr (kN == 4) {
+        switch (warps_for(a.d / 8, kN)) {
+            case 3: return launch_fwd<3>(k_norm_fwd_vec<kN, 3>, a, s);
+            case 5: return launch_fwd<5>(k_norm_fwd_vec<kN, 5>, a, s);
+            case 6: return launch_fwd<6>(k_norm_fwd_vec<kN, 6>, a, s);
+            case 7: return launch_fwd<7>(k_norm_fwd_vec<kN, 7>, a, s);
+            default: break;
+        }
+    }
+    return launch_fwd<32>(k_norm_fwd_vec<kN, 32>, a, s);
 }
 
 // Ring kernels: one piece a lane up to 256 columns, two beyond, as long as 16
-// warps hold a row; nw = 0: they do not.
-static RingShape ring_shape(int32_t d, bool shift, int warps, int* pieces) {
+// warps hold a row; nw = 0: they do not.  `three`: three pieces where that makes
+// two groups out of one, whose exchanges then hide each other (forward, 13,107 x
+// 5,120: 59.6 us with two, 52.6 with three; 10,923 x 6,144: 53.9, 50.6).  The
+// backward pass would spill registers (86.9, 146.9).
+static RingShape ring_shape(int32_t d, bool shift, bool three, int* pieces) {
     const int nv = (d + 7) / 8 + (shift ? 1 : 0);        // a row may reach into one chunk more
+    constexpr int warps = kRingThreads / 32;
     *pieces = nv <= 32 ? 1 : 2;
     RingShape sh = {(nv + 32 * *pieces - 1) / (32 * *pieces), 0};
-    if (sh.nw > 16) sh.nw = 0;
+    if (three && sh.nw > warps / 2 && nv <= warps / 2 * 96) {
+        *pieces = 3;
+        sh.nw = (nv + 95) / 96;
+    }
+    if (sh.nw > warps) sh.nw = 0;
     else sh.groups = warps / sh.nw < 15 || sh.nw == 1 ? warps / sh.nw : 15;   // a barrier for each
     return sh;
 }
@@ -1092,20 +1112,28 @@ static dlm_status_t launch_ring(const Args& a, RingShape sh, unsigned grid, cuda
     return launch_pdl(kKern, dim3(grid), dim3(threads), size_t(kSlots) * threads * 16, s, what, a, sh);
 }
 
-template <int kN, bool kShift>
-static dlm_status_t launch_fwd_ring(const NormFwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
-    return launch_ring<k_norm_fwd_ring<kN, kShift>, 2 * kN * kFwdStages>(a, sh, grid, s, "k_norm_fwd launch");
+template <bool kShift>
+static dlm_status_t launch_fwd_ring(int pieces, const NormFwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
+    const char* what = "k_norm_fwd launch";
+    switch (pieces) {
+        case 1: return launch_ring<k_norm_fwd_ring<1, kShift>, 2 * fwd_stages<1>()>(a, sh, grid, s, what);
+        case 2: return launch_ring<k_norm_fwd_ring<2, kShift>, 4 * fwd_stages<2>()>(a, sh, grid, s, what);
+        default: return launch_ring<k_norm_fwd_ring<3, kShift>, 6 * fwd_stages<3>()>(a, sh, grid, s, what);
+    }
 }
 
-template <int kN, bool kShift>
-static dlm_status_t launch_bwd_ring(const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
-    constexpr int kSlots = 2 * kN * bwd_stages<kN>();
+template <int kFormat, bool kShift>
+static dlm_status_t launch_bwd_ring(int pieces, const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
     const char* what = "k_norm_bwd launch";
-    if (a.format == DLM_PACK_NONE)
-        return launch_ring<k_norm_bwd_ring<kN, DLM_PACK_NONE, kShift>, kSlots>(a, sh, grid, s, what);
-    if (a.format == DLM_PACK_INT8)
-        return launch_ring<k_norm_bwd_ring<kN, DLM_PACK_INT8, kShift>, kSlots>(a, sh, grid, s, what);
-    return launch_ring<k_norm_bwd_ring<kN, DLM_PACK_E4M3, kShift>, kSlots>(a, sh, grid, s, what);
+    return pieces == 1 ? launch_ring<k_norm_bwd_ring<1, kFormat, kShift>, 2 * bwd_stages<1>()>(a, sh, grid, s, what)
+                       : launch_ring<k_norm_bwd_ring<2, kFormat, kShift>, 4 * bwd_stages<2>()>(a, sh, grid, s, what);
+}
+
+template <bool kShift>
+static dlm_status_t launch_bwd_ring(int pieces, const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
+    return a.format == DLM_PACK_NONE ? launch_bwd_ring<DLM_PACK_NONE, kShift>(pieces, a, sh, grid, s)
+         : a.format == DLM_PACK_INT8 ? launch_bwd_ring<DLM_PACK_INT8, kShift>(pieces, a, sh, grid, s)
+                                     : launch_bwd_ring<DLM_PACK_E4M3, kShift>(pieces, a, sh, grid, s);
 }
 
 static unsigned ring_grid(int64_t rows) { return unsigned(rows < 148 ? rows : 148); }
@@ -1187,24 +1215,24 @@ extern "C" dlm_status_t dlm_norm_fwd(const uint16_t* x, int64_t rows, int32_t d_
     const bool vec = d_model % 8 == 0 && ld_x % 8 == 0 && ld_y % 8 == 0 && aligned16(x) && aligned16(y) &&
                      param_aligned(weight) && param_aligned(bias) && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
     int pieces = 0;
-    RingShape sh = ring_shape(d_model, false, kRingThreads / 32, &pieces);
+    RingShape sh = ring_shape(d_model, false, true, &pieces);
     if (vec) {
         const int nv = d_model / 8;
         const int64_t all = rows * nv;                   // 16-byte pieces of the call
         if (sh.nw && all >= kRingPieces && pack_format == DLM_PACK_NONE)
-            return pieces == 1 ? launch_fwd_ring<1, false>(a, sh, ring_grid(rows), s)
-                               : launch_fwd_ring<2, false>(a, sh, ring_grid(rows), s);
-        if (all <= kOnePiece && warps_for(nv, 1)) return launch_fwd_vec<1>(warps_for(nv, 1), a, s);
-        if (all <= kTwoPieces && warps_for(nv, 2)) return launch_fwd_vec<2>(warps_for(nv, 2), a, s);
-        if (warps_for(nv, 4)) return launch_fwd_vec<4>(warps_for(nv, 4), a, s);
+            return launch_fwd_ring<false>(pieces, a, sh, ring_grid(rows), s);
+        // (rows of up to 256 or 512 columns fill a warp by one or two pieces a lane: 262,147 x 256 with the
+        // checkpoint 92 us, with four pieces 165)
+        if ((all <= kOnePiece || nv <= 32) && warps_for(nv, 1)) return launch_fwd_vec<1>(a, s);
+        if ((all <= kTwoPieces || nv <= 64) && warps_for(nv, 2)) return launch_fwd_vec<2>(a, s);
+        if (warps_for(nv, 4)) return launch_fwd_vec<4>(a, s);
     }
     // rows of x and y in step with one another, if not with the 16-byte borders
     const bool shift = aligned16(x) && aligned16(y) && (ld_x - ld_y) % 8 == 0;
-    sh = ring_shape(d_model, true, kRingThreads / 32, &pieces);
+    sh = ring_shape(d_model, true, true, &pieces);
     const RingShape any = any_shape(d_model);
     if (shift && sh.nw)
-        st = pieces == 1 ? launch_fwd_ring<1, true>(a, sh, shift_grid(rows, sh), s)
-                         : launch_fwd_ring<2, true>(a, sh, shift_grid(rows, sh), s);
+        st = launch_fwd_ring<true>(pieces, a, sh, shift_grid(rows, sh), s);
     else if (any.nw) st = launch_any<k_norm_fwd_any>(a, any, 1, s, "k_norm_fwd launch");
     else st = launch_pdl(k_norm_fwd_wide, dim3(unsigned(rows < 148 * 4 ? rows : 148 * 4)), dim3(kWideThreads), 0, s,
                          "k_norm_fwd_wide launch", a);
@@ -1255,7 +1283,7 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
                            (a.x ? aligned16(x) && (ld_dy - ld_x) % 8 == 0
                                 : (reinterpret_cast<uintptr_t>(q) & 7) == 0 && (ld_dy - d_model) % 8 == 0);
         int pieces = 0;
-        const RingShape sh = ring_shape(d_model, !vec, kRingThreads / 32, &pieces), any = any_shape(d_model);
+        const RingShape sh = ring_shape(d_model, !vec, false, &pieces), any = any_shape(d_model);
         const bool ring = (vec || shift) && sh.nw;
         // (a group's rows are `groups` apart then: in step only if that is a multiple of 8)
         if (ring && rows <= (vec || sh.groups % 8 == 0 ? int64_t(kAloneRows) * sh.groups : sh.groups)) {
@@ -1263,10 +1291,10 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
             alone = true;
         }
         if (vec && sh.nw) {
-            st = pieces == 1 ? launch_bwd_ring<1, false>(a, sh, p.grid, s) : launch_bwd_ring<2, false>(a, sh, p.grid, s);
+            st = launch_bwd_ring<false>(pieces, a, sh, p.grid, s);
         } else if (shift && sh.nw) {
             if (!alone) p.grid = shift_grid(rows, sh);
-            st = pieces == 1 ? launch_bwd_ring<1, true>(a, sh, p.grid, s) : launch_bwd_ring<2, true>(a, sh, p.grid, s);
+            st = launch_bwd_ring<true>(pieces, a, sh, p.grid, s);
         } else if (any.nw) {
             const char* what = "k_norm_bwd launch";
             st = pack_format == DLM_PACK_NONE ? launch_any<k_norm_bwd_any<DLM_PACK_NONE>>(a, any, 2, s, what)

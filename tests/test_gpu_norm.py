@@ -98,6 +98,22 @@ def test_row_counts(r, d):
 
 
 @pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("d", [256, 264, 512, 520, 1288, 2560, 3336, 4104, 4608, 5120, 6144, 6152, 7168])
+def test_many_rows_either_side_of_the_split_rules(d, fmt):
+    """One, two and three pieces a lane, every number of warps up to 8, and
+    widths that fill the last warp or leave most of it without work; one row
+    short of and past the size from which the rings take over."""
+    for r in (-(-148 * 4608 * 8 // d) - 1, -(-148 * 4608 * 8 // d) + 41):
+        x, w, b, dy = _make(r, d, bf16, 0.0, d + fmt)
+        kind = RMS if d % 3 == 1 else LAYER
+        out = dlm.norm_fwd(x, w, b, 1e-5, kind, pack=fmt)
+        _check_fwd(out, x, w, b, 1e-5, kind == RMS, 0.0)
+        if fmt:
+            q, s = ref.pack(x, fmt)
+            assert torch.equal(out.packed.q.cpu(), q) and torch.equal(out.packed.scale.cpu(), s)
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
 @pytest.mark.parametrize("d", [65, 500, 1501, 2001, 3003, 5001, 8100])
 def test_many_rows_off_the_16_byte_borders(d, fmt):
     """Rows in step with one another but not with the borders, several to a
