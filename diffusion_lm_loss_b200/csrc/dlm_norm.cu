@@ -404,7 +404,13 @@ struct Pieces {
     }
 };
 
-template <int kN, bool kShift>
+// kMean: what is subtracted is known to be the mean (kSubtract) or nothing
+// (kNothing), or is asked for (kAsk, nothing being subtracted as zero).  On
+// 16-byte borders RMS norm runs faster as kAsk, however odd (13,107 x 5,120: 44 us
+// against 46, 8,192 x 8,192: 43, 47); off them the work that kNothing saves
+// counts (13,419 x 5,001: 72, 64).  Layer norm as kAsk: 46.7 against 46.1.
+enum Mean { kSubtract, kNothing, kAsk };
+template <int kN, bool kShift, Mean kMean>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a, RingShape sh) {
     constexpr int kS = fwd_stages<kN>(), kR = 2;                // two rows at a time: their exchanges share barriers
     extern __shared__ uint4 ring_mem[];
@@ -470,14 +476,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
                 for (int k = 0; k < 4; ++k) f[r][j][k] = f2bf16(u[k]);
                 if (kShift && pc.edge[j]) pc.clip(j, a.d, f[r][j]);
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) sum = f2add(sum, f[r][j][k]);
+                for (int k = 0; k < 4; ++k)
+                    if (kMean != kNothing) sum = f2add(sum, f[r][j][k]);
             }
             f2unpack(sum, lo, hi);
             s1[r] = lo + hi;
         }
         ring.step(ring.get);
         issue();
-        if (a.rms) s1[0] = s1[1] = 0.f;
+        if (kMean == kNothing || (kMean == kAsk && a.rms)) s1[0] = s1[1] = 0.f;
         else group_sum2<!kShift>(s1[0], s1[1], &s_x[par][0][g * sh.nw], wg, sh, 1 + g);
         #pragma unroll
         for (int r = 0; r < kR; ++r) {
@@ -487,8 +494,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
             for (int j = 0; j < kN; ++j) {
                 const uint64_t nm = f2splat(pc.in[j] ? -s1[r] : 0.f);
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) f[r][j][k] = f2add(f[r][j][k], nm);
-                if (kShift && pc.edge[j]) pc.clip(j, a.d, f[r][j]);
+                for (int k = 0; k < 4; ++k)
+                    if (kMean != kNothing) f[r][j][k] = f2add(f[r][j][k], nm);
+                if (kMean != kNothing && kShift && pc.edge[j]) pc.clip(j, a.d, f[r][j]);
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) sq = f2fma(f[r][j][k], f[r][j][k], sq);
             }
@@ -501,7 +509,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
             if (n <= r) break;
             const float rstd = rsqrtf(s2[r] * inv_d + a.eps);
             if (t == 0) {
-                if (!a.rms) a.mean[row + r * step] = s1[r];
+                if (kMean == kSubtract || (kMean == kAsk && !a.rms)) a.mean[row + r * step] = s1[r];
                 a.rstd[row + r * step] = rstd;
             }
             const uint64_t r2 = f2splat(rstd);
@@ -517,17 +525,22 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(NormFwdArgs a
     cp_async_wait<0>();
 }
 
-// kFormat: DLM_PACK_NONE (x itself) or the format of its checkpoint
-template <int kN, int kFormat, bool kShift>
+// kFormat: DLM_PACK_NONE (x itself) or the format of its checkpoint.  kLean: RMS
+// norm whose bias gradient is not wanted: three packed operations a pair less
+// (16,384 x 4,096: 69.3 -> 68.3 us, from 8 bits 75.5 -> 65.9; 13,419 x 5,001: 114 -> 88).
+template <int kN, int kFormat, bool kShift, bool kLean>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a, RingShape sh) {
     constexpr int kS = bwd_stages<kN>();
     constexpr bool kHeld8 = kFormat != DLM_PACK_NONE;
+    // when a row's place in the ring is filled again: with little to compute, after the exchange (kLean, 13,107 x
+    // 5,120: 85.4 us before it, 80.6 after; from 8 bits 80.7, 82.4; not kLean, 26,214 x 2,560: 70.0, 71.6)
+    constexpr bool kLate = kLean && !kShift && !kHeld8;
     extern __shared__ uint4 ring_mem[];                   // ring of dy, x pieces; at the end the groups' sums
     __shared__ float2 s_x[2][16];                         // [row parity][warp]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = warp / sh.nw, wg = warp - g * sh.nw;
     const int t = wg * 32 + lane, gt = sh.nw * 32;
-    uint64_t w[kN][4], dw[kN][4], db[kN][4];
+    uint64_t w[kN][4], dw[kN][4], db[kLean ? 1 : kN][4];
     const int64_t first = int64_t(g) * gridDim.x + blockIdx.x, step = int64_t(sh.groups) * gridDim.x;
     const int phase = kShift ? int((first * a.ld_dy) & 7) : 0;
     const Pieces<kN, kShift> pc(t, gt, a.d, phase);
@@ -579,7 +592,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
         two[j] = kShift && pc.in[j] && (pc.c[j] & 127) > 120 && (pc.c[j] | 127) + 1 < a.d ? 128 - (pc.c[j] & 127) : 8;
     auto next_stats = [&](bool more) {
         if (!more) return;
-        if (!a.rms) mean_n = __ldg(pmean);
+        if (!kLean && !a.rms) mean_n = __ldg(pmean);
         rstd_n = __ldg(prstd);
         pmean += step;
         prstd += step;
@@ -600,7 +613,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     for (int j = 0; j < kN; ++j) {
         pc.params(j, a.d, a.w, a.param_f32, 1.f, a.w ? a.offset : 0.f, w[j]);
         #pragma unroll
-        for (int k = 0; k < 4; ++k) dw[j][k] = db[j][k] = 0;
+        for (int k = 0; k < 4; ++k) dw[j][k] = db[kLean ? 0 : j][k] = 0;
     }
     const float inv_d = 1.0f / float(a.d);
     uint16_t* pdx = a.dx + first * a.ld_dx + t * 8 - phase;
@@ -624,19 +637,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
                 const uint2 q2 = lds8(ring.get + (2 * j + 1) * ring.pitch);
                 unpack_codes(q2.x, kFormat, xh[j][0], xh[j][1]);
                 unpack_codes(q2.y, kFormat, xh[j][2], xh[j][3]);
-                // code * scale - mean in one FMA: the held value is not rounded
+                // code * scale - mean in one FMA: the held value is not rounded (kLean: the code times
+                // scale * rstd)
+                const float f1 = kLean ? qs[j] * rstd : qs[j], f2 = kLean ? qs2[j] * rstd : qs2[j];
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint64_t s = f2splat(qs[j]);
-                    if (kShift && two[j] < 8)
-                        s = f2pack(2 * k < two[j] ? qs[j] : qs2[j], 2 * k + 1 < two[j] ? qs[j] : qs2[j]);
-                    xh[j][k] = f2fma(xh[j][k], s, nm);
+                    uint64_t s = f2splat(f1);
+                    if (kShift && two[j] < 8) s = f2pack(2 * k < two[j] ? f1 : f2, 2 * k + 1 < two[j] ? f1 : f2);
+                    xh[j][k] = kLean ? f2mul(xh[j][k], s) : f2fma(xh[j][k], s, nm);
                 }
             } else {
                 const uint4 x4 = lds16(ring.get + (2 * j + 1) * ring.pitch);
                 const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) xh[j][k] = f2add(f2bf16(xw[k]), nm);
+                for (int k = 0; k < 4; ++k) xh[j][k] = kLean ? f2mul(f2bf16(xw[k]), r2) : f2add(f2bf16(xw[k]), nm);
             }
             uint64_t dy4[4];
             #pragma unroll
@@ -648,29 +662,34 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
             #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint64_t dy = dy4[k];
-                xh[j][k] = f2mul(xh[j][k], r2);
+                if (!kLean) xh[j][k] = f2mul(xh[j][k], r2);
                 gr[j][k] = f2mul(dy, w[j][k]);
-                s1 = f2add(s1, gr[j][k]);
                 s2 = f2fma(gr[j][k], xh[j][k], s2);
                 dw[j][k] = f2fma(dy, xh[j][k], dw[j][k]);
-                db[j][k] = f2add(db[j][k], dy);
+                if constexpr (!kLean) {
+                    s1 = f2add(s1, gr[j][k]);
+                    db[j][k] = f2add(db[j][k], dy);
+                }
             }
         }
         ring.step(ring.get);
-        issue();
+        if (!kLate) issue();
         float lo, hi, v1, v2;
         f2unpack(s1, lo, hi);
         v1 = lo + hi;
         f2unpack(s2, lo, hi);
         v2 = lo + hi;
-        group_sum2<false>(v1, v2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
+        if constexpr (kLean) v2 = group_sum1(v2, reinterpret_cast<float*>(&s_x[par][g * sh.nw]), wg, sh, 1 + g);
+        else group_sum2<false>(v1, v2, &s_x[par][g * sh.nw], wg, sh, 1 + g);
+        if (kLate) issue();
         const float by = -rstd * inv_d;
         const uint64_t n1 = f2splat(a.rms ? 0.f : v1 * by), n2 = f2splat(v2 * by);
         #pragma unroll
         for (int j = 0; j < kN; ++j) {
             uint64_t o[4];
             #pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = f2fma(gr[j][k], r2, f2fma(xh[j][k], n2, n1));
+            for (int k = 0; k < 4; ++k)
+                o[k] = f2fma(gr[j][k], r2, kLean ? f2mul(xh[j][k], n2) : f2fma(xh[j][k], n2, n1));
             pc.store(j, a.d, pdx + j * gt * 8, o);
         }
     }
@@ -683,10 +702,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     #pragma unroll
     for (int j = 0; j < kN; ++j) {
         #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < (kLean ? 1 : 2); ++h) {
             uint64_t* p = reinterpret_cast<uint64_t*>(acc + (2 * g + h) * wide + (j * gt + t) * 8);
             #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = h ? db[j][i] : dw[j][i];
+            for (int i = 0; i < 4; ++i) p[i] = h ? db[kLean ? 0 : j][i] : dw[j][i];
         }
     }
     __syncthreads();
@@ -696,7 +715,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
         for (int k = 0; k < sh.groups; ++k) {
             const int at = 2 * k * wide + c + (kShift ? int(((int64_t(k) * gridDim.x + blockIdx.x) * a.ld_dy) & 7) : 0);
             sw += acc[at];
-            sb += acc[at + wide];
+            if (!kLean) sb += acc[at + wide];
         }
         if (gridDim.x == 1) {                             // the whole sum: no k_norm_join
             put_grad(a.d_weight, c, sw, a.grad_f32, a.accumulate);
@@ -1112,21 +1131,32 @@ static dlm_status_t launch_ring(const Args& a, RingShape sh, unsigned grid, cuda
     return launch_pdl(kKern, dim3(grid), dim3(threads), size_t(kSlots) * threads * 16, s, what, a, sh);
 }
 
+template <int kN, bool kShift>
+static dlm_status_t launch_fwd_ring(const NormFwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
+    const char* what = "k_norm_fwd launch";
+    constexpr int kSlots = 2 * kN * fwd_stages<kN>();
+    return a.rms ? launch_ring<k_norm_fwd_ring<kN, kShift, kShift ? kNothing : kAsk>, kSlots>(a, sh, grid, s, what)
+                 : launch_ring<k_norm_fwd_ring<kN, kShift, kSubtract>, kSlots>(a, sh, grid, s, what);
+}
+
 template <bool kShift>
 static dlm_status_t launch_fwd_ring(int pieces, const NormFwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
-    const char* what = "k_norm_fwd launch";
-    switch (pieces) {
-        case 1: return launch_ring<k_norm_fwd_ring<1, kShift>, 2 * fwd_stages<1>()>(a, sh, grid, s, what);
-        case 2: return launch_ring<k_norm_fwd_ring<2, kShift>, 4 * fwd_stages<2>()>(a, sh, grid, s, what);
-        default: return launch_ring<k_norm_fwd_ring<3, kShift>, 6 * fwd_stages<3>()>(a, sh, grid, s, what);
-    }
+    return pieces == 1 ? launch_fwd_ring<1, kShift>(a, sh, grid, s)
+         : pieces == 2 ? launch_fwd_ring<2, kShift>(a, sh, grid, s) : launch_fwd_ring<3, kShift>(a, sh, grid, s);
+}
+
+template <int kN, int kFormat, bool kShift>
+static dlm_status_t launch_bwd_ring(const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
+    const char* what = "k_norm_bwd launch";
+    constexpr int kSlots = 2 * kN * bwd_stages<kN>();
+    if (a.rms && !a.d_bias) return launch_ring<k_norm_bwd_ring<kN, kFormat, kShift, true>, kSlots>(a, sh, grid, s, what);
+    return launch_ring<k_norm_bwd_ring<kN, kFormat, kShift, false>, kSlots>(a, sh, grid, s, what);
 }
 
 template <int kFormat, bool kShift>
 static dlm_status_t launch_bwd_ring(int pieces, const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
-    const char* what = "k_norm_bwd launch";
-    return pieces == 1 ? launch_ring<k_norm_bwd_ring<1, kFormat, kShift>, 2 * bwd_stages<1>()>(a, sh, grid, s, what)
-                       : launch_ring<k_norm_bwd_ring<2, kFormat, kShift>, 4 * bwd_stages<2>()>(a, sh, grid, s, what);
+    return pieces == 1 ? launch_bwd_ring<1, kFormat, kShift>(a, sh, grid, s)
+                       : launch_bwd_ring<2, kFormat, kShift>(a, sh, grid, s);
 }
 
 template <bool kShift>

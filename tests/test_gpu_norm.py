@@ -133,6 +133,21 @@ def test_many_rows_off_the_16_byte_borders(d, fmt):
     _check_bwd(got, dy, held, out.mean, out.rstd, w, False, 0.0, f32)
 
 
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("d", [1, 8, 65, 129, 256, 264, 500, 1003, 2048, 2056, 4096, 4104, 5001, 8192])
+@pytest.mark.parametrize("r", [1, 2, 30, 150, 1301])
+def test_rms_without_a_bias(r, d, fmt):
+    x, w, _, dy = _make(r, d, f32 if d % 2 else bf16, 0.0, d + r + fmt, shift=0.5)
+    out = dlm.norm_fwd(x, w, None, 1e-6, RMS, pack=fmt)
+    _check_fwd(out, x, w, None, 1e-6, True, 0.0)
+    got = dlm.norm_bwd(dy, out.packed if fmt else x, out.rstd, None, w, RMS, grad_dtype=f32)
+    held = ref.held(*ref.pack(x, fmt), fmt, torch.float64).cuda() if fmt else x
+    _check_bwd(got, dy, held, None, out.rstd, w, True, 0.0, f32, bias=False)
+    old = torch.randn(d, device="cuda")
+    acc = dlm.norm_bwd(dy, out.packed if fmt else x, out.rstd, None, w, RMS, d_weight=old.clone(), accumulate=True)
+    assert torch.equal(acc.d_x, got.d_x) and torch.equal(acc.d_weight, old + got.d_weight)
+
+
 @pytest.mark.parametrize("d,ld", [(1000, 1003), (1001, 1001), (264, 264), (77, 85)])
 @pytest.mark.parametrize("shift", [0, 1, 8])
 @pytest.mark.parametrize("r", [1, 2, 400])
