@@ -22,7 +22,10 @@
 // walks over its rows while asynchronous copies fill a ring of the next ones
 // in shared memory, each thread copying just the pieces that it will read
 // itself, so that the loads need no barrier of their own and no wait but the
-// copy group's.  A row stays in registers between its sums and its output.
+// copy group's.  A row stays in registers between its sums and its output.  Where
+// the width leaves room for one group only, nothing works while it exchanges its
+// sums: there the forward pass takes three pieces a lane (two groups again), the
+// backward pass two rows at a time (k_norm_bwd_two).
 // Backward: the columns' dw and db stay in fp32 registers over all rows of a
 // group; a CTA leaves one partial row, and k_norm_join adds the partial rows
 // in a fixed order.  x comes as bf16 or from its 8-bit checkpoint.
@@ -274,6 +277,29 @@ __device__ __forceinline__ void group_sum2(float& s1, float& s2, float2* slot, i
     const float other = __shfl_xor_sync(~0u, v, 16);
     s1 = lane < 16 ? v : other;
     s2 = lane < 16 ? other : v;
+}
+
+// The same for two rows in one exchange: lanes 8 q .. 8 q + 7 carry sum q of
+// s1[0], s1[1], s2[0], s2[1].  slot: [nw] float4.
+__device__ __forceinline__ void group_sum4(float (&s1)[2], float (&s2)[2], float4* slot, int wg, const RingShape sh,
+                                           int bar) {
+    const int lane = threadIdx.x & 31;
+    const bool up = lane & 16, odd = lane & 8;
+    const float a0 = (up ? s2[0] : s1[0]) + __shfl_xor_sync(~0u, up ? s1[0] : s2[0], 16);
+    const float a1 = (up ? s2[1] : s1[1]) + __shfl_xor_sync(~0u, up ? s1[1] : s2[1], 16);
+    float v = (odd ? a1 : a0) + __shfl_xor_sync(~0u, odd ? a0 : a1, 8);
+    #pragma unroll
+    for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    if ((lane & 7) == 0) reinterpret_cast<float*>(slot + wg)[lane >> 3] = v;
+    named_barrier_sync(bar, sh.nw * 32);
+    const float* from = reinterpret_cast<const float*>(slot + (lane & 7)) + (lane >> 3);
+    v = ((lane & 7) < sh.nw ? from[0] : 0.f) + ((lane & 7) + 8 < sh.nw ? from[32] : 0.f);
+    #pragma unroll
+    for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    s1[0] = __shfl_sync(~0u, v, 0);
+    s1[1] = __shfl_sync(~0u, v, 8);
+    s2[0] = __shfl_sync(~0u, v, 16);
+    s2[1] = __shfl_sync(~0u, v, 24);
 }
 
 __device__ __forceinline__ float group_sum1(float v, float* slot, int wg, const RingShape sh, int bar) {
@@ -727,6 +753,188 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(NormBwdArgs a
     }
 }
 
+// The same for rows on 16-byte borders that leave room for one group of 9 to 12
+// warps on an SM: no other group works while it exchanges its sums, so it takes
+// two rows at a time, which its warps have the registers for (168 a lane).
+// 13,107 x 5,120: 86 -> 73 us, RMS 81 -> 66, RMS from 8 bits 81 -> 67.  (Layer
+// norm from 8 bits got slower, 98 -> 114, and stays with one row.  Two groups with
+// two rows each, the weight in shared memory and dy read again for want of
+// registers: 16,384 x 4,096 95 us instead of 71.)
+constexpr int kTwoThreads = 384, kTwoStages = 8;
+
+template <int kFormat, bool kLean>
+__global__ void __launch_bounds__(kTwoThreads, 1) k_norm_bwd_two(NormBwdArgs a, RingShape sh) {
+    constexpr int kN = 2, kS = kTwoStages, kR = 2;
+    constexpr bool kHeld8 = kFormat != DLM_PACK_NONE;
+    extern __shared__ uint4 ring_mem[];
+    __shared__ float4 s_x[2][kTwoThreads / 32];
+    const int t = threadIdx.x, wg = t >> 5, gt = sh.nw * 32;
+    const int64_t first = blockIdx.x, step = gridDim.x;
+    const Pieces<kN, false> pc(t, gt, a.d, 0);
+    Ring<kS, 2 * kN> ring(ring_mem);
+    #pragma unroll
+    for (int j = 0; j < 2 * kN; ++j)
+        if (!pc.in[j / 2]) ring.clear(ring_mem, j);
+    pdl_wait();
+    pdl_launch_dependents();
+    int n = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
+    const int nb = (a.d + DLM_PACK_BLOCK - 1) / DLM_PACK_BLOCK;
+    const uint16_t* pdy = a.dy + first * a.ld_dy + t * 8;
+    const uint16_t* px = kHeld8 ? nullptr : a.x + first * a.ld_x + t * 8;
+    const uint8_t* pq = kHeld8 ? a.q + first * a.d + t * 8 : nullptr;
+    int left = n;
+    auto issue = [&]() {
+        if (left > 0) {
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                if (!pc.in[j]) continue;
+                const uint32_t dst = ring.put + 2 * j * ring.pitch;
+                cp_async16(dst, pdy + j * gt * 8);
+                if constexpr (kHeld8) cp_async8(dst + ring.pitch, pq + j * gt * 8);
+                else cp_async16(dst + ring.pitch, px + j * gt * 8);
+            }
+            pdy += step * a.ld_dy;
+            if constexpr (kHeld8) pq += step * a.d;
+            else px += step * a.ld_x;
+            --left;
+        }
+        cp_async_commit();
+        ring.step(ring.put);
+    };
+    // statistics and block factors of the rows after those in work
+    const float* pmean = a.mean + first;
+    const float* prstd = a.rstd + first;
+    const float* pqs = kHeld8 ? a.q_scale + first * nb : nullptr;
+    float mean_n[kR] = {}, rstd_n[kR], qs_n[kR][kN];
+    auto next_stats = [&](int rows) {
+        #pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            if (r >= rows) break;
+            if (!kLean && !a.rms) mean_n[r] = __ldg(pmean);
+            rstd_n[r] = __ldg(prstd);
+            pmean += step;
+            prstd += step;
+            if constexpr (kHeld8) {
+                #pragma unroll
+                for (int j = 0; j < kN; ++j) qs_n[r][j] = pc.in[j] ? __ldg(pqs + pc.c[j] / DLM_PACK_BLOCK) : 0.f;
+                pqs += step * nb;
+            }
+        }
+    };
+    #pragma unroll 1
+    for (int s = 0; s < kS - 1; ++s) issue();
+    next_stats(n);
+    uint64_t w[kN][4], dw[kN][4], db[kLean ? 1 : kN][4];
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        pc.params(j, a.d, a.w, a.param_f32, 1.f, a.w ? a.offset : 0.f, w[j]);
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) dw[j][k] = db[kLean ? 0 : j][k] = 0;
+    }
+    const float inv_d = 1.0f / float(a.d);
+    uint16_t* pdx = a.dx + first * a.ld_dx + t * 8;
+    int par = 0;
+    for (; n > 0; n -= kR, par ^= 1) {
+        float rstd[kR], mean[kR], qs[kR][kN];
+        #pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            rstd[r] = rstd_n[r];
+            mean[r] = mean_n[r];
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) qs[r][j] = kHeld8 ? qs_n[r][j] : 0.f;
+        }
+        next_stats(n - kR);
+        cp_async_wait<kS - 1 - kR>();
+        uint64_t xh[kR][kN][4], gr[kR][kN][4];
+        float v1[kR], v2[kR];
+        #pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            v1[r] = v2[r] = 0.f;
+            if (r >= n) break;
+            const uint64_t nm = f2splat(-mean[r]), r2 = f2splat(rstd[r]);
+            uint64_t s1 = 0, s2 = 0;
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                const uint4 y4 = lds16(ring.get + 2 * j * ring.pitch);
+                const uint32_t yw[4] = {y4.x, y4.y, y4.z, y4.w};
+                if constexpr (kHeld8) {
+                    const uint2 q2 = lds8(ring.get + (2 * j + 1) * ring.pitch);
+                    unpack_codes(q2.x, kFormat, xh[r][j][0], xh[r][j][1]);
+                    unpack_codes(q2.y, kFormat, xh[r][j][2], xh[r][j][3]);
+                    const uint64_t s = f2splat(kLean ? qs[r][j] * rstd[r] : qs[r][j]);
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) xh[r][j][k] = kLean ? f2mul(xh[r][j][k], s) : f2fma(xh[r][j][k], s, nm);
+                } else {
+                    const uint4 x4 = lds16(ring.get + (2 * j + 1) * ring.pitch);
+                    const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        xh[r][j][k] = kLean ? f2mul(f2bf16(xw[k]), r2) : f2add(f2bf16(xw[k]), nm);
+                }
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t dy = f2bf16(yw[k]);
+                    if (!kLean) xh[r][j][k] = f2mul(xh[r][j][k], r2);
+                    gr[r][j][k] = f2mul(dy, w[j][k]);
+                    s2 = f2fma(gr[r][j][k], xh[r][j][k], s2);
+                    dw[j][k] = f2fma(dy, xh[r][j][k], dw[j][k]);
+                    if constexpr (!kLean) {
+                        s1 = f2add(s1, gr[r][j][k]);
+                        db[j][k] = f2add(db[j][k], dy);
+                    }
+                }
+            }
+            ring.step(ring.get);
+            float lo, hi;
+            f2unpack(s1, lo, hi);
+            v1[r] = lo + hi;
+            f2unpack(s2, lo, hi);
+            v2[r] = lo + hi;
+        }
+        issue();
+        group_sum4(v1, v2, s_x[par], wg, sh, 1);
+        issue();                                              // (into a slot whose pieces the sums have used)
+        #pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            if (r >= n) break;
+            const float by = -rstd[r] * inv_d;
+            const uint64_t r2 = f2splat(rstd[r]), n1 = f2splat(a.rms ? 0.f : v1[r] * by), n2 = f2splat(v2[r] * by);
+            #pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                uint64_t o[4];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[k] = f2fma(gr[r][j][k], r2, kLean ? f2mul(xh[r][j][k], n2) : f2fma(xh[r][j][k], n2, n1));
+                pc.store(j, a.d, pdx + j * gt * 8, o);
+            }
+            pdx += step * a.ld_dx;
+        }
+    }
+    cp_async_wait<0>();
+    // one group: a thread's columns are its own
+    float* part = a.part + int64_t(blockIdx.x) * 2 * a.pitch;
+    #pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        if (!pc.in[j]) continue;
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = pc.c[j] + 2 * k;
+            float w0, w1, b0, b1;
+            f2unpack(dw[j][k], w0, w1);
+            f2unpack(db[kLean ? 0 : j][k], b0, b1);
+            if (gridDim.x == 1) {                             // the whole sum: no k_norm_join
+                put_grad(a.d_weight, c, w0, a.grad_f32, a.accumulate);
+                put_grad(a.d_weight, c + 1, w1, a.grad_f32, a.accumulate);
+                put_grad(a.d_bias, c, b0, a.grad_f32, a.accumulate);
+                put_grad(a.d_bias, c + 1, b1, a.grad_f32, a.accumulate);
+            } else {
+                if (a.d_weight) *reinterpret_cast<float2*>(part + c) = make_float2(w0, w1);
+                if (a.d_bias) *reinterpret_cast<float2*>(part + a.pitch + c) = make_float2(b0, b1);
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // rows that are not on 16-byte borders
 // ---------------------------------------------------------------------------
@@ -1122,11 +1330,11 @@ static RingShape ring_shape(int32_t d, bool shift, bool three, int* pieces) {
     return sh;
 }
 
-// kSlots: a thread's 16-byte slots in shared memory
-template <auto kKern, int kSlots, typename Args>
+// kSlots: a thread's 16-byte slots in shared memory; kThreads: the kernel's bound
+template <auto kKern, int kSlots, int kThreads, typename Args>
 static dlm_status_t launch_ring(const Args& a, RingShape sh, unsigned grid, cudaStream_t s, const char* what) {
     const unsigned threads = unsigned(sh.nw * sh.groups * 32);
-    dlm_status_t st = allow_smem<kKern, kSlots * kRingThreads * 16>(what);
+    dlm_status_t st = allow_smem<kKern, kSlots * kThreads * 16>(what);
     if (st != DLM_OK) return st;
     return launch_pdl(kKern, dim3(grid), dim3(threads), size_t(kSlots) * threads * 16, s, what, a, sh);
 }
@@ -1135,8 +1343,8 @@ template <int kN, bool kShift>
 static dlm_status_t launch_fwd_ring(const NormFwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
     const char* what = "k_norm_fwd launch";
     constexpr int kSlots = 2 * kN * fwd_stages<kN>();
-    return a.rms ? launch_ring<k_norm_fwd_ring<kN, kShift, kShift ? kNothing : kAsk>, kSlots>(a, sh, grid, s, what)
-                 : launch_ring<k_norm_fwd_ring<kN, kShift, kSubtract>, kSlots>(a, sh, grid, s, what);
+    return a.rms ? launch_ring<k_norm_fwd_ring<kN, kShift, kShift ? kNothing : kAsk>, kSlots, kRingThreads>(a, sh, grid, s, what)
+                 : launch_ring<k_norm_fwd_ring<kN, kShift, kSubtract>, kSlots, kRingThreads>(a, sh, grid, s, what);
 }
 
 template <bool kShift>
@@ -1145,18 +1353,23 @@ static dlm_status_t launch_fwd_ring(int pieces, const NormFwdArgs& a, RingShape 
          : pieces == 2 ? launch_fwd_ring<2, kShift>(a, sh, grid, s) : launch_fwd_ring<3, kShift>(a, sh, grid, s);
 }
 
-template <int kN, int kFormat, bool kShift>
+template <int kN, int kFormat, bool kShift, bool kLean>
 static dlm_status_t launch_bwd_ring(const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
     const char* what = "k_norm_bwd launch";
-    constexpr int kSlots = 2 * kN * bwd_stages<kN>();
-    if (a.rms && !a.d_bias) return launch_ring<k_norm_bwd_ring<kN, kFormat, kShift, true>, kSlots>(a, sh, grid, s, what);
-    return launch_ring<k_norm_bwd_ring<kN, kFormat, kShift, false>, kSlots>(a, sh, grid, s, what);
+    if constexpr (kN == 2 && !kShift && (kLean || kFormat == DLM_PACK_NONE))
+        if (sh.groups == 1 && sh.nw * 32 <= kTwoThreads)
+            return launch_ring<k_norm_bwd_two<kFormat, kLean>, 4 * kTwoStages, kTwoThreads>(a, sh, grid, s, what);
+    return launch_ring<k_norm_bwd_ring<kN, kFormat, kShift, kLean>, 2 * kN * bwd_stages<kN>(), kRingThreads>(a, sh, grid,
+                                                                                                             s, what);
 }
 
 template <int kFormat, bool kShift>
 static dlm_status_t launch_bwd_ring(int pieces, const NormBwdArgs& a, RingShape sh, unsigned grid, cudaStream_t s) {
-    return pieces == 1 ? launch_bwd_ring<1, kFormat, kShift>(a, sh, grid, s)
-                       : launch_bwd_ring<2, kFormat, kShift>(a, sh, grid, s);
+    if (a.rms && !a.d_bias)
+        return pieces == 1 ? launch_bwd_ring<1, kFormat, kShift, true>(a, sh, grid, s)
+                           : launch_bwd_ring<2, kFormat, kShift, true>(a, sh, grid, s);
+    return pieces == 1 ? launch_bwd_ring<1, kFormat, kShift, false>(a, sh, grid, s)
+                       : launch_bwd_ring<2, kFormat, kShift, false>(a, sh, grid, s);
 }
 
 template <bool kShift>

@@ -111,6 +111,12 @@ def test_many_rows_either_side_of_the_split_rules(d, fmt):
         if fmt:
             q, s = ref.pack(x, fmt)
             assert torch.equal(out.packed.q.cpu(), q) and torch.equal(out.packed.scale.cpu(), s)
+        # backward, an odd and an even number of rows for each group
+        for n in (r, 148 * 3 + 1, 148 * 2, 2, 1):
+            got = dlm.norm_bwd(dy[:n], x[:n], out.rstd[:n], None if kind == RMS else out.mean[:n], w, kind,
+                               want_d_bias=kind == LAYER, grad_dtype=f32)
+            _check_bwd(got, dy[:n], x[:n], None if kind == RMS else out.mean[:n], out.rstd[:n], w, kind == RMS, 0.0, f32,
+                       bias=kind == LAYER)
 
 
 @pytest.mark.parametrize("fmt", [0, 1, 2])
@@ -134,7 +140,7 @@ def test_many_rows_off_the_16_byte_borders(d, fmt):
 
 
 @pytest.mark.parametrize("fmt", [0, 1, 2])
-@pytest.mark.parametrize("d", [1, 8, 65, 129, 256, 264, 500, 1003, 2048, 2056, 4096, 4104, 5001, 8192])
+@pytest.mark.parametrize("d", [1, 8, 65, 129, 256, 264, 500, 1003, 2048, 2056, 4096, 4104, 5001, 5120, 6144, 6152, 8192])
 @pytest.mark.parametrize("r", [1, 2, 30, 150, 1301])
 def test_rms_without_a_bias(r, d, fmt):
     x, w, _, dy = _make(r, d, f32 if d % 2 else bf16, 0.0, d + r + fmt, shift=0.5)
