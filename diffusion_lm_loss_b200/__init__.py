@@ -414,6 +414,15 @@ class LinearOut:
         return device_status(self.workspace)
 
 
+def _new(dev, dtype: torch.dtype, rows: int, cols: Optional[int] = None) -> torch.Tensor:
+    """An uninitialised contiguous tensor [rows] or [rows, cols] on device
+    `dev` (empty_strided: 0.8 us a tensor less than torch.empty, 0.4 less than
+    new_empty)."""
+    if cols is None:
+        return torch.empty_strided((rows,), (1,), dtype=dtype, device=dev)
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
+
+
 def _aligned_workspace(nbytes: int, device, align: int = 1024) -> torch.Tensor:
     """A uint8 workspace whose first byte is `align`-byte aligned (the loss
     needs 256, the fused head 1024; the caching allocator guarantees 512 and
@@ -421,7 +430,7 @@ def _aligned_workspace(nbytes: int, device, align: int = 1024) -> torch.Tensor:
     slightly larger buffer, which the slice keeps alive.  (Two buffers are never
     held at once, and one as large as the fused head's is asked for once.)"""
     if align <= 512:
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
         if buf.data_ptr() % align == 0:
             return buf
         del buf
@@ -691,7 +700,7 @@ def embed_fwd(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: fl
     if not _all_on(dev, ids, out, dev_status, pad):
         _on_cuda(ids=ids, weight=weight, out=out, dev_status=dev_status, pad_mask=pad)
     if out is None:
-        out = weight.new_empty((T, D))
+        out = _new(weight.device, torch.bfloat16, T, D)
     _call(dev, "dlm_embed_fwd", ctypes.byref(layout), ids.data_ptr(), weight.data_ptr(), ld_w, V, D, scale,
           out.data_ptr(), ld_out, _ptr(dev_status))
     return out
@@ -734,7 +743,7 @@ def embed_bwd(layout: Layout, ids: torch.Tensor, d_out: torch.Tensor, vocab: int
     if not _all_on(dev, ids, d_weight, workspace, pad):
         _on_cuda(ids=ids, d_out=d_out, d_weight=d_weight, workspace=workspace, pad_mask=pad)
     if d_weight is None:
-        d_weight = d_out.new_empty((vocab, D), dtype=grad_dtype)
+        d_weight = _new(d_out.device, grad_dtype, vocab, D)
     if workspace is None:
         workspace = _aligned_workspace(embed_bwd_workspace_size(layout, D, vocab), d_out.device, 256)
     _call(dev, "dlm_embed_bwd", ctypes.byref(layout), ids.data_ptr(), d_out.data_ptr(), ld, vocab, D, scale, gt,
@@ -755,8 +764,7 @@ class Packed8:
 
 
 def _empty_packed(rows: int, cols: int, fmt: int, dev) -> Packed8:
-    return Packed8(torch.empty((rows, cols), dtype=torch.uint8, device=dev),
-                   torch.empty((rows, -(-cols // PACK_BLOCK)), dtype=torch.float32, device=dev), fmt)
+    return Packed8(_new(dev, torch.uint8, rows, cols), _new(dev, torch.float32, rows, -(-cols // PACK_BLOCK)), fmt)
 
 
 def _check_packed(p: Packed8, rows: int, cols: int, name: str):
@@ -798,7 +806,7 @@ def unpack8(packed: Packed8, out: Optional[torch.Tensor] = None) -> torch.Tensor
     if not _all_on(dev, packed.scale, out):
         _on_cuda(q=packed.q, scale=packed.scale, out=out)
     if out is None:
-        out = packed.q.new_empty((rows, cols), dtype=torch.bfloat16)
+        out = _new(packed.q.device, torch.bfloat16, rows, cols)
     _call(dev, "dlm_unpack8", packed.q.data_ptr(), packed.scale.data_ptr(), rows, cols, packed.format, out.data_ptr(),
           ld)
     return out
@@ -857,8 +865,8 @@ def norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optio
         if not _all_on(x.get_device(), weight, bias):
             _on_cuda(x=x, weight=weight, bias=bias)
         pk = _empty_packed(rows, D, pack, x.device) if pack != PACK_NONE else None
-        out = NormOut(x.new_empty((rows, D)), x.new_empty(rows, dtype=torch.float32) if layer else None,
-                      x.new_empty(rows, dtype=torch.float32), pk)
+        out = NormOut(_new(x.device, torch.bfloat16, rows, D), _new(x.device, torch.float32, rows) if layer else None,
+                      _new(x.device, torch.float32, rows), pk)
     _call(x.get_device(), "dlm_norm_fwd", x.data_ptr(), rows, D, ld, _ptr(weight), _ptr(bias), pt, kind, eps,
           weight_offset, out.y.data_ptr(), ld_y, out.mean.data_ptr() if layer else None, out.rstd.data_ptr(), pack,
           pk.q.data_ptr() if pk is not None else None, pk.scale.data_ptr() if pk is not None else None)
@@ -928,11 +936,11 @@ def norm_bwd(d_y: torch.Tensor, x, rstd: torch.Tensor, mean: Optional[torch.Tens
         _on_cuda(d_y=d_y, x=xs, q=q, scale=qs, mean=mean if layer else None, rstd=rstd, weight=weight, d_x=d_x,
                  d_weight=d_weight, d_bias=d_bias, workspace=workspace)
     if d_x is None:
-        d_x = d_y.new_empty((rows, D))
+        d_x = _new(d_y.device, torch.bfloat16, rows, D)
     if want_w and d_weight is None:
-        d_weight = d_y.new_empty(D, dtype=grad_dtype)
+        d_weight = _new(d_y.device, grad_dtype, D)
     if want_b and d_bias is None:
-        d_bias = d_y.new_empty(D, dtype=grad_dtype)
+        d_bias = _new(d_y.device, grad_dtype, D)
     if workspace is None:
         workspace = _aligned_workspace(norm_bwd_workspace_size(rows, D), d_y.device, 256)
     _call(dev, "dlm_norm_bwd", d_y.data_ptr(), ld_dy, _ptr(xs), ld_x, fmt, _ptr(q), _ptr(qs),

@@ -386,7 +386,8 @@ def test_no_second_workspace_is_asked_for_while_one_is_held(monkeypatch):
     returns."""
     empty, alive, asked, most = torch.empty, [], [], []
 
-    def off_border(n, **kw):
+    def off_border(n, *stride, **kw):
+        n = n[0] if stride else n                    # empty_strided((n,), (1,)) or empty(n)
         buf = empty(n + 8192, **kw)
         at = (-buf.data_ptr()) % 4096 + 16           # on a 16-byte border only
         buf = buf[at:at + n]
@@ -395,6 +396,7 @@ def test_no_second_workspace_is_asked_for_while_one_is_held(monkeypatch):
         most.append(sum(r() is not None for r in alive[:-1]))
         return buf
     monkeypatch.setattr(torch, "empty", off_border)
+    monkeypatch.setattr(torch, "empty_strided", off_border)
     for align, requests in ((1024, 1), (256, 2)):
         alive.clear(), asked.clear(), most.clear()
         ws = dlm._aligned_workspace(5000, "cpu", align)
