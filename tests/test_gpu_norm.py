@@ -301,6 +301,29 @@ def test_nan_and_infinity_stay_in_their_row(d):
     assert bool(torch.isfinite(got.d_x[good]).all()) and bool(torch.isnan(got.d_x[4]).all())
 
 
+@pytest.mark.parametrize("kind", [LAYER, RMS])
+@pytest.mark.parametrize("d", [256, 1024, 4096, 5001, 5120, 6144, 8192])
+def test_nan_and_infinity_stay_in_their_row_of_many(d, kind):
+    """Rows that share a turn, an exchange of sums and a chunk of memory with
+    one that is not finite."""
+    r = -(-148 * 4608 * 8 // d) + 5
+    x, w, _, dy = _make(r, d, bf16, 0.0, 9)
+    rows = torch.tensor([0, 148, 149, 296, r // 2, r - 1], device="cuda")
+    clean = dlm.norm_fwd(x, w, None, kind=kind)
+    want = dlm.norm_bwd(dy, x, clean.rstd, clean.mean, w, kind)
+    bad = x.clone()
+    bad[rows[::2], d - 1] = float("nan")
+    bad[rows[1::2], 0] = float("inf")
+    good = torch.ones(r, dtype=torch.bool, device="cuda")
+    good[rows] = False
+    out = dlm.norm_fwd(bad, w, None, kind=kind)
+    assert torch.equal(out.y[good], clean.y[good]) and torch.equal(out.rstd[good], clean.rstd[good])
+    assert bool(torch.isnan(out.y[rows[::2]]).all())
+    got = dlm.norm_bwd(dy, bad, out.rstd, out.mean, w, kind)
+    assert torch.equal(got.d_x[good], want.d_x[good])
+    assert bool(torch.isnan(got.d_x[rows[::2]]).all()) and bool(torch.isnan(got.d_weight[d - 1]))
+
+
 def test_rows_past_two_to_the_31_elements():
     ld = 2 ** 30 + 8
     buf = torch.zeros(2 * ld + 512, dtype=bf16, device="cuda")
