@@ -841,7 +841,8 @@ def norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optio
              out: Optional[NormOut] = None) -> NormOut:
     """Layer norm or RMS norm of the rows of x (bf16 [rows, d_model]; see
     dlm_norm_fwd).  pack: also x in 8 bits, which norm_bwd takes in x's place.
-    Reuses the buffers of `out` when given."""
+    Reuses the buffers of `out` when given; what comes back holds only what
+    this call wrote."""
     rows, D = _shape2(x, "x")
     ld = _check_rows(x, torch.bfloat16, "x", rows, D)
     pt = _check_params(weight, bias, D)
@@ -861,6 +862,7 @@ def norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optio
             _check_packed(pk, rows, D, "out.packed")
         _on_cuda(x=x, weight=weight, bias=bias, y=out.y, mean=out.mean if layer else None, rstd=out.rstd,
                  q=pk.q if pk is not None else None, scale=pk.scale if pk is not None else None)
+        out = NormOut(out.y, out.mean if layer else None, out.rstd, pk)
     else:
         if not _all_on(x.get_device(), weight, bias):
             _on_cuda(x=x, weight=weight, bias=bias)
