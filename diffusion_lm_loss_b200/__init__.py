@@ -1104,15 +1104,17 @@ def decision_loss(logits: torch.Tensor, vocab: int, cand_off: torch.Tensor, cand
 class _EmbedFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, layout, ids, scale):
-        ctx.save_for_backward(ids)
+        ctx.save_for_backward(ids, _pad_mask(layout))         # both are read again, as they are now
         ctx.args = (layout, weight.shape[0], scale)
         return embed_fwd(layout, ids, weight, scale)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        (ids,) = ctx.saved_tensors
+        ids, pad = ctx.saved_tensors
         layout, vocab, scale = ctx.args
+        if pad is not None:                                   # saved-tensor hooks may give another tensor back
+            layout = make_layout(layout.n_units, layout.seq_len, layout._tensors[0], pad, layout.n_tokens)
         return (embed_bwd(layout, ids, _as_rows(grad), vocab, scale).d_weight,) + (None,) * 3
 
 

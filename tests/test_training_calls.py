@@ -30,3 +30,51 @@ def test_a_reused_norm_result_reports_this_call_alone(calls):
     assert rms.mean is None and rms.packed is None, "the means of the call before"
     again = dlm.norm_fwd(x, pack=dlm.PACK_INT8, out=dlm.NormOut(*buffers))
     assert again.packed is buffers[3] and again.mean is buffers[1]
+
+
+@pytest.fixture
+def plain_embedding(monkeypatch):
+    """embed over plain CPU forms of its two calls."""
+    def fwd(layout, ids, weight, scale=1.0, out=None, dev_status=None):
+        pad = dlm._pad_mask(layout)
+        y = weight[ids.long().clamp(0, weight.shape[0] - 1)] * scale
+        return y if pad is None else y * (pad == 0)[:, None]
+
+    def bwd(layout, ids, d_out, vocab, scale=1.0, **kw):
+        pad = dlm._pad_mask(layout)
+        assert layout.pad_mask == (None if pad is None else pad.data_ptr())
+        keep = d_out if pad is None else d_out * (pad == 0)[:, None]
+        dw = torch.zeros(vocab, d_out.shape[1]).index_add_(0, ids.long(), keep.float() * scale)
+        return dlm.EmbedGrad(dw.to(bf16), torch.empty(0, dtype=torch.uint8))
+    monkeypatch.setattr(dlm, "_on_cuda", lambda **kw: None)
+    monkeypatch.setattr(dlm, "embed_fwd", fwd)
+    monkeypatch.setattr(dlm, "embed_bwd", bwd)
+
+
+def _embedding_inputs():
+    pad = torch.tensor([0, 1, 0, 0, 0, 1], dtype=torch.uint8)
+    ids = torch.tensor([1, 2, 1, 0, 4, 4], dtype=torch.int32)
+    w = torch.ones(5, 3, dtype=bf16, requires_grad=True)
+    return pad, ids, w, dlm.make_layout(1, 6, None, pad)
+
+
+def test_a_pad_mask_changed_before_backward_is_refused(plain_embedding):
+    pad, ids, w, lay = _embedding_inputs()
+    y = dlm.embed(lay, ids, w)
+    pad.zero_()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    for lay in (lay, dlm.make_layout(1, 6)):                 # a mask left alone, and none
+        w.grad = None
+        dlm.embed(lay, ids, w).sum().backward()
+        assert w.grad[:, 0].tolist() == [1, 2, 1, 0, 2]
+
+
+def test_backward_takes_the_pad_mask_that_was_saved(plain_embedding):
+    """Saved-tensor hooks (here: copies) may hand back another tensor."""
+    pad, ids, w, lay = _embedding_inputs()
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(), lambda t: t):
+        y = dlm.embed(lay, ids, w)
+    pad.zero_()
+    y.sum().backward()
+    assert w.grad[:, 0].tolist() == [1, 2, 0, 0, 1]
