@@ -1103,10 +1103,10 @@ def decision_loss(logits: torch.Tensor, vocab: int, cand_off: torch.Tensor, cand
 
 class _EmbedFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, weight, layout, ids, scale):
+    def forward(ctx, weight, layout, ids, scale, dev_status):
         ctx.save_for_backward(ids, _pad_mask(layout))         # both are read again, as they are now
         ctx.args = (layout, weight.shape[0], scale)
-        return embed_fwd(layout, ids, weight, scale)
+        return embed_fwd(layout, ids, weight, scale, dev_status=dev_status)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -1115,16 +1115,18 @@ class _EmbedFn(torch.autograd.Function):
         layout, vocab, scale = ctx.args
         if pad is not None:                                   # saved-tensor hooks may give another tensor back
             layout = make_layout(layout.n_units, layout.seq_len, layout._tensors[0], pad, layout.n_tokens)
-        return (embed_bwd(layout, ids, _as_rows(grad), vocab, scale).d_weight,) + (None,) * 3
+        return (embed_bwd(layout, ids, _as_rows(grad), vocab, scale).d_weight,) + (None,) * 4
 
 
-def embed(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+def embed(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
+          dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """embed_fwd as a differentiable function of `weight`; its gradient is
     dense, bf16 [vocab, d_model] (embed_bwd can add it to another one).
+    dev_status as there: the one place where an id outside the table shows.
     To capture a whole backward pass in a CUDA graph, drop every earlier eager
     graph of the same parameters first (torch's own rule), or capture embed_bwd
     and norm_bwd, which have no such state."""
-    return _EmbedFn.apply(weight, layout, ids, scale)
+    return _EmbedFn.apply(weight, layout, ids, scale, dev_status)
 
 
 class _NormFn(torch.autograd.Function):

@@ -78,3 +78,15 @@ def test_backward_takes_the_pad_mask_that_was_saved(plain_embedding):
     pad.zero_()
     y.sum().backward()
     assert w.grad[:, 0].tolist() == [1, 2, 0, 0, 1]
+
+
+def test_embed_hands_its_status_word_to_the_forward_call(calls):
+    ids, w = torch.zeros(6, dtype=torch.int32), torch.zeros(5, 3, dtype=bf16, requires_grad=True)
+    lay = dlm.make_layout(1, 6)
+    status = torch.zeros(1, dtype=torch.int32)
+    dlm.embed(lay, ids, w, 2.0, dev_status=status)
+    dlm.embed(lay, ids, w, 2.0)
+    assert [name for name, _ in calls] == ["dlm_embed_fwd"] * 2
+    assert [args[-1] for _, args in calls] == [status.data_ptr(), None]
+    with pytest.raises(ValueError, match="dev_status"):
+        dlm.embed(lay, ids, w, dev_status=torch.zeros(1))
