@@ -1157,4 +1157,8 @@ def norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[
     keep8 = PACK_INT8 or PACK_E4M3: x is kept for the backward pass in 8 bits,
     written by the forward kernel, in place of x itself; the backward pass then
     takes those values for x (mean and rstd stay those of x)."""
-    return _NormFn.apply(x, weight, bias, eps, kind, weight_offset, keep8)
+    if keep8 not in (PACK_NONE, PACK_INT8, PACK_E4M3):
+        raise ValueError("keep8: PACK_NONE, PACK_INT8 or PACK_E4M3")
+    # under no_grad a parameter still says that it needs a gradient, and inside the function gradients are
+    # always off: asked for here, so that no form is written that nobody reads
+    return _NormFn.apply(x, weight, bias, eps, kind, weight_offset, keep8 if torch.is_grad_enabled() else PACK_NONE)

@@ -90,3 +90,25 @@ def test_embed_hands_its_status_word_to_the_forward_call(calls):
     assert [args[-1] for _, args in calls] == [status.data_ptr(), None]
     with pytest.raises(ValueError, match="dev_status"):
         dlm.embed(lay, ids, w, dev_status=torch.zeros(1))
+
+
+def test_norm_keeps_nothing_in_8_bits_where_no_gradient_is_recorded(calls):
+    x = torch.zeros(4, 200, dtype=bf16)
+    w = torch.zeros(200, dtype=bf16, requires_grad=True)
+
+    def formats():
+        out = [args[-3] for name, args in calls if name == "dlm_norm_fwd"]
+        calls.clear()
+        return out
+    dlm.norm(x, w, keep8=dlm.PACK_INT8)
+    with torch.no_grad():
+        dlm.norm(x, w, keep8=dlm.PACK_INT8)
+    with torch.inference_mode():
+        dlm.norm(x, w, keep8=dlm.PACK_E4M3)
+    dlm.norm(x, w.detach(), keep8=dlm.PACK_INT8)
+    with torch.no_grad(), torch.enable_grad():
+        dlm.norm(x, w, keep8=dlm.PACK_E4M3)
+    assert formats() == [dlm.PACK_INT8, 0, 0, 0, dlm.PACK_E4M3]
+    for off in (False, True):                                # refused all the same
+        with torch.set_grad_enabled(not off), pytest.raises(ValueError, match="keep8"):
+            dlm.norm(x, w, keep8=5)
