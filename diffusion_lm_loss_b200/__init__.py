@@ -281,6 +281,17 @@ def _ok(code: int, where: str):
         raise DlmError(code, where, detail)
 
 
+def _call(dev: int, name: str, *args):
+    """A library call on the current stream of CUDA device `dev`, which becomes
+    the current device for it (-1: of the current one)."""
+    fn = getattr(_lib or lib(), name)
+    if dev >= 0 and dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            _ok(fn(*args, _stream()), name)
+    else:
+        _ok(fn(*args, _stream()), name)
+
+
 def _check_out(loss: torch.Tensor, unit_loss: Optional[torch.Tensor], layout: Layout,
                workspace: torch.Tensor):
     """The scalar outputs and the workspace of a reused result object (the
@@ -609,27 +620,16 @@ def decision_loss_fwd_bwd(logits: torch.Tensor, vocab: int, cand_off: torch.Tens
 
 
 def device_status(workspace: torch.Tensor) -> int:
-    """Device status word of a loss workspace (synchronises the stream)."""
+    """Device status word of a workspace (synchronises the current stream of
+    its device)."""
     v = ctypes.c_uint32(0)
-    _ok(lib().dlm_get_device_status(_ptr(workspace), ctypes.byref(v), _stream()),
-        "dlm_get_device_status")
+    _call(workspace.get_device(), "dlm_get_device_status", workspace.data_ptr(), ctypes.byref(v))
     return int(v.value)
 
 
 # --------------------------------------------------------------------------
 # embedding, norm, activations in 8 bits
 # --------------------------------------------------------------------------
-def _call(dev: int, name: str, *args):
-    """A library call on the current stream of CUDA device `dev`, which becomes
-    the current device for it (-1: of the current one)."""
-    fn = getattr(_lib or lib(), name)
-    if dev >= 0 and dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
-            _ok(fn(*args, _stream()), name)
-    else:
-        _ok(fn(*args, _stream()), name)
-
-
 def _all_on(dev: int, *tensors) -> bool:
     """Whether these (None = not given) are on CUDA device `dev`: the quick
     form of _on_cuda, which words what is wrong where it is not so."""

@@ -112,3 +112,41 @@ def test_norm_keeps_nothing_in_8_bits_where_no_gradient_is_recorded(calls):
     for off in (False, True):                                # refused all the same
         with torch.set_grad_enabled(not off), pytest.raises(ValueError, match="keep8"):
             dlm.norm(x, w, keep8=5)
+
+
+def test_device_status_reads_on_the_workspace_s_own_device(monkeypatch):
+    """The call that wrote the word ran on its tensors' device and on that
+    device's stream: the reading has to wait for that stream."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.dev
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    class Workspace:
+        def get_device(self):
+            return 1
+
+        def data_ptr(self):
+            return 4096
+
+    class Lib:
+        @staticmethod
+        def dlm_get_device_status(ws, word, stream):
+            seen.append((ws, stream))
+            word._obj.value = 5
+            return 0
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(dlm, "_stream", lambda: ("stream of", current[0]))
+    monkeypatch.setattr(dlm, "_lib", Lib)
+    assert dlm.device_status(Workspace()) == 5
+    current[0] = 1
+    assert dlm.device_status(Workspace()) == 5
+    assert seen == [(4096, ("stream of", 1))] * 2
