@@ -658,9 +658,19 @@ def _check_rows(t: Optional[torch.Tensor], dtype, name: str, rows: int, cols: in
     return ld
 
 
+def _in_32_bits(*sizes: int):
+    """Sizes that the C ABI takes as int32 (ctypes would cut larger ones to
+    their low bits)."""
+    for n in sizes:
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"a size of {n}: columns and table rows are counted in 32 bits")
+
+
 def _shape2(t: torch.Tensor, name: str):
+    """(rows, columns) of a matrix."""
     if t.dim() != 2:
         raise ValueError(f"{name}: must be 2-D, got shape {tuple(t.shape)}")
+    _in_32_bits(t.shape[1])
     return t.shape
 
 
@@ -692,6 +702,7 @@ def embed_fwd(layout: Layout, ids: torch.Tensor, weight: torch.Tensor, scale: fl
     V, D = weight.shape if weight.dim() == 2 else (0, 0)
     if V < 1 or D < 1:
         raise ValueError("weight: [vocab, d_model]")
+    _in_32_bits(V, D)
     ld_w = _check_rows(weight, torch.bfloat16, "weight", V, D)
     if dev_status is not None and (dev_status.dtype not in (torch.int32, torch.uint32) or dev_status.numel() < 1):
         raise ValueError("dev_status: an int32 / uint32 tensor of at least one element")
@@ -716,6 +727,7 @@ class EmbedGrad:
 
 
 def embed_bwd_workspace_size(layout: Layout, d_model: int, vocab: int) -> int:
+    _in_32_bits(d_model, vocab)
     return int(lib().dlm_embed_bwd_workspace_size(ctypes.byref(layout), d_model, vocab))
 
 
@@ -730,6 +742,7 @@ def embed_bwd(layout: Layout, ids: torch.Tensor, d_out: torch.Tensor, vocab: int
     D = d_out.shape[1] if d_out.dim() == 2 else 1
     if D < 1 or vocab < 1:
         raise ValueError("d_out and the table need at least one column and one row")
+    _in_32_bits(D, vocab)
     ld = _check_rows(d_out, torch.bfloat16, "d_out", T, D)
     if accumulate and d_weight is None:
         raise ValueError("accumulate needs d_weight")
@@ -885,6 +898,7 @@ class NormGrad:
 
 @functools.lru_cache(maxsize=256)      # of the sizes alone
 def norm_bwd_workspace_size(rows: int, d_model: int) -> int:
+    _in_32_bits(d_model)
     return int(lib().dlm_norm_bwd_workspace_size(rows, d_model))
 
 

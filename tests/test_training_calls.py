@@ -150,3 +150,27 @@ def test_device_status_reads_on_the_workspace_s_own_device(monkeypatch):
     current[0] = 1
     assert dlm.device_status(Workspace()) == 5
     assert seen == [(4096, ("stream of", 1))] * 2
+
+
+def test_sizes_past_32_bits_are_refused_and_not_cut_to_their_low_bits(calls):
+    """The library counts columns and table rows in 32 bits, and ctypes cuts what
+    does not fit: 2^32 + 256 columns would have come back as 256, the rest of the
+    output never written.  (Shapes without memory: nothing is allocated.)"""
+    def big(rows, cols, dtype=bf16):
+        return torch.empty((rows, cols), dtype=dtype, device="meta")
+    n = 2 ** 32 + 256
+    ids, lay = torch.zeros(4, dtype=torch.int32), dlm.make_layout(1, 4)
+    x, r = big(1, n), torch.zeros(1)
+    p = dlm.Packed8(big(1, n, torch.uint8), big(1, n // 128, torch.float32), dlm.PACK_INT8)
+    for size in (n, 2 ** 31):
+        for fn in (lambda: dlm.embed_bwd_workspace_size(lay, size, 50), lambda: dlm.embed_bwd_workspace_size(lay, 8, size),
+                   lambda: dlm.norm_bwd_workspace_size(4, size),
+                   lambda: dlm.embed_bwd(lay, ids, torch.zeros(4, 8, dtype=bf16), size)):
+            with pytest.raises(ValueError, match="32 bits"):
+                fn()
+    for fn in (lambda: dlm.embed_fwd(lay, ids, big(n, 2)), lambda: dlm.embed_fwd(lay, ids, big(3, n)),
+               lambda: dlm.embed_bwd(lay, ids, big(4, n), 50), lambda: dlm.pack8(x), lambda: dlm.unpack8(p),
+               lambda: dlm.norm_fwd(x), lambda: dlm.norm_bwd(x, p, r, r), lambda: dlm.norm_bwd(x, x, r, r)):
+        with pytest.raises(ValueError, match="32 bits"):
+            fn()
+    assert not calls
