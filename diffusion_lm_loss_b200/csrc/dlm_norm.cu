@@ -1548,7 +1548,7 @@ extern "C" dlm_status_t dlm_norm_bwd(const uint16_t* d_y, int64_t ld_dy, const u
         }
         if (st != DLM_OK) return st;
     }
-    if ((!d_weight && !d_bias) || alone) return DLM_OK;
+    if ((!d_weight && !d_bias) || alone || (rows == 0 && accumulate)) return DLM_OK;
     return launch_pdl(k_norm_join, dim3(unsigned((d_model + 31) / 32), 2), dim3(kNormJoinWarps * 32), 0, s,
                       "k_norm_join launch", (const float*)a.part, int(p.grid), p.pitch, d_model,
                       int(grad_dtype == DLM_F32), accumulate, d_weight, d_bias);

@@ -5,6 +5,8 @@ import pytest
 import torch
 
 import diffusion_lm_loss_b200 as dlm
+from diffusion_lm_loss_b200 import build as dlm_build
+from test_host_failures import _a_device_may_be_usable
 
 bf16 = torch.bfloat16
 
@@ -174,3 +176,24 @@ def test_sizes_past_32_bits_are_refused_and_not_cut_to_their_low_bits(calls):
         with pytest.raises(ValueError, match="32 bits"):
             fn()
     assert not calls
+
+
+def test_no_rows_to_accumulate_launch_nothing():
+    """d_weight and d_bias are left as they are, bit for bit: adding zeros would
+    turn -0 into 0.  (The device check is passed over, so that a launch would
+    fail for want of a device.)"""
+    if _a_device_may_be_usable():
+        pytest.skip("a CUDA device may be usable here: the hook must not run with fake pointers")
+    dlm_build.build()
+    L = dlm.lib()
+    assert L.dlm_test_skip_device_check(1) == 0
+    try:
+        n = L.dlm_norm_bwd_workspace_size(0, 64)
+
+        def bwd(accumulate, dw, db):
+            return L.dlm_norm_bwd(None, 64, None, 64, 0, None, None, None, None, None, 0, 0, 0.0, 0, 64, None, 64, 0,
+                                  accumulate, dw, db, 1 << 20, n, None)
+        assert bwd(1, 4096, 8192) == 0 and bwd(1, 4096, None) == 0 and bwd(0, None, None) == 0
+        assert bwd(0, 4096, None) == 4                     # zeros are written: a launch
+    finally:
+        assert L.dlm_test_skip_device_check(0) == 0
