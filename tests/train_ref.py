@@ -146,3 +146,77 @@ def assert_within(got, want, bound, what=""):
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside, worst at {k}: got "
                              f"{got.reshape(-1)[k].item()!r}, want {want.reshape(-1)[k].item()!r}, bound "
                              f"{bound.expand_as(want).reshape(-1)[k].item()!r}")
+
+
+# --------------------------------------------------------------------------
+# Bounds by the additions that a term really goes through, in place of all of
+# its row's or column's (the bounds above): for long rows only these see a
+# single lost or doubled term.
+# --------------------------------------------------------------------------
+def embed_links(n, tokens):
+    """Additions on the way of a term in a table row of n tokens (n: a tensor),
+    the most over the kernels: 32 in a chunk (of 8 to 32 tokens); a warp's share
+    of the row's chunks, of which there are n / 8 + 2 at most, and 16 warps.  Calls
+    of up to 1,024 tokens may take one launch: an eighth of the row's part of
+    the list, and 8 warps."""
+    long = 32 + torch.ceil((n / 8 + 2) / 16) + 16
+    if tokens <= 1024:
+        long = torch.maximum(long, torch.full_like(n, 128 + 8))
+    return torch.minimum(n, long)
+
+
+def embed_grad_tight(ids, dw, mag, dtype, pad=None):
+    """embed_links additions, the scale's product, one more addition where the
+    sums are added to a gradient, the output's rounding."""
+    kept = ids.long() if pad is None else ids.long()[pad == 0]
+    n = torch.bincount(kept, minlength=dw.shape[0]).double()[:, None]
+    return ((embed_links(n, ids.numel()) + 2) * U * mag + HALF[dtype] * dw.abs()) * 1.01 + 1e-40
+
+
+def norm_links(rows):
+    """Additions on the way of a term of dw or db: the rows of a group (144 CTAs
+    at least where there are that many rows; two rows in the single-CTA calls),
+    up to 16 groups of a CTA, 148 partial rows in 16 shares of up to 10, and
+    the 16 shares."""
+    return max(2, -(-rows // 144)) + 16 + 10 + 16
+
+
+def norm_grad_tight(dy, x, mean, rstd, w, rms, offset, dtype):
+    """norm_grad_bounds with norm_links additions: xh has 2 roundings, its
+    product with dy one."""
+    dx, dw, db = norm_grad(dy, x, mean, rstd, w, rms, offset)
+    bx, _, _ = norm_grad_bounds(dy, x, mean, rstd, w, rms, offset, dtype)
+    dy, x = dy.double(), x.double()
+    xh = ((x - (0.0 if rms else mean.double()[:, None])) * rstd.double()[:, None]).abs()
+    n = (norm_links(x.shape[0]) + 3) * U
+    h = HALF[dtype]
+    return (bx, (n * (dy.abs() * xh).sum(0) + h * dw.abs()) * 1.01 + 1e-40,
+            (n * dy.abs().sum(0) + h * db.abs()) * 1.01 + 1e-40)
+
+
+# --------------------------------------------------------------------------
+# Inputs whose sums are exact in fp32 in any order: small integers (times powers
+# of two), of which 2^24 units are never reached.  A term lost or counted twice
+# shows whatever the length.
+# --------------------------------------------------------------------------
+def integers(shape, top, g, device, zero=False):
+    """Whole numbers -top..top, zero left out unless asked for."""
+    v = torch.randint(1, top + 1, shape, generator=g, device=device)
+    v = torch.where(torch.rand(shape, generator=g, device=device) < 0.5, -v, v)
+    if zero:
+        v = torch.where(torch.rand(shape, generator=g, device=device) < 0.2, torch.zeros_like(v), v)
+    return v
+
+
+def exact_norm_inputs(r, d, fmt, g, device):
+    """dy, x (bf16), held (64 bits), q, scale, mean, rstd: dy xh are multiples of
+    1/8 below 4 x (8 + 3) / 2 = 22, so 176 units: 95,000 rows stay below 2^24."""
+    x = integers((r, d), 8, g, device, zero=True).to(torch.bfloat16)
+    dy = integers((r, d), 4, g, device).to(torch.bfloat16)
+    mean = integers((r,), 3, g, device, zero=True).float()
+    rstd = 2.0 ** -torch.randint(1, 3 if fmt == 0 else 2, (r,), generator=g, device=device).float()
+    if fmt == 0:
+        return dy, x, x.double(), None, None, mean, rstd
+    codes = x.to(torch.int8).view(torch.uint8) if fmt == INT8 else x.float().to(torch.float8_e4m3fn).view(torch.uint8)
+    scale = 2.0 ** -torch.randint(0, 3, (r, -(-d // BLOCK)), generator=g, device=device).float()
+    return dy, None, held(codes, scale, fmt, torch.float64), codes, scale, mean, rstd
