@@ -1127,7 +1127,7 @@ class _EmbedFn(torch.autograd.Function):
     def backward(ctx, grad):
         ids, pad = ctx.saved_tensors
         layout, vocab, scale = ctx.args
-        if pad is not None:                                   # saved-tensor hooks may give another tensor back
+        if pad is not None and pad.data_ptr() != layout.pad_mask:        # saved-tensor hooks gave another one back
             layout = make_layout(layout.n_units, layout.seq_len, layout._tensors[0], pad, layout.n_tokens)
         return (embed_bwd(layout, ids, _as_rows(grad), vocab, scale).d_weight,) + (None,) * 4
 
