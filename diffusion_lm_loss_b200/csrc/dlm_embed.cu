@@ -757,13 +757,28 @@ __global__ void __launch_bounds__(kSmallWarps * 32) k_embed_small(EmbSmallArgs a
 }
 
 // Workspace of the gradient: header, row_start [vocab + 1], order and sid
-// [n_tokens], partials.
+// [n_tokens], partials; and the CTAs of its launches, but for those that write zeros.
 struct EmbPlan {
     int chunk;
     int64_t chunks;
     int pitch;
     size_t off_start, off_order, off_sid, off_part, bytes;
+    unsigned threads;     // of a CTA of k_embed_grad
+    int tiles, join_tiles, zero_split;
+    int64_t join_ctas, small_ctas;
 };
+
+// The CTAs that write zeros, by the bytes of a row of the gradient.
+struct EmbZeros { int rows; int64_t grad, join; };
+
+static EmbZeros embed_zeros(const EmbPlan& p, int32_t vocab, int64_t row_bytes) {
+    EmbZeros z;
+    z.rows = row_bytes >= kZeroBytes ? 1 : row_bytes * 32 <= kZeroBytes ? 32 : int(kZeroBytes / row_bytes);
+    const int64_t per_grad = z.rows * int64_t(p.threads / 32), per_join = z.rows * int64_t(kJoinWarps);
+    z.grad = (p.zero_split + per_grad - 1) / per_grad;
+    z.join = (vocab - p.zero_split + per_join - 1) / per_join;
+    return z;
+}
 
 static bool embed_plan(const dlm_layout_t* L, int32_t vocab, int32_t d, EmbPlan* p) {
     if (!layout_ok(L) || vocab < 1 || d < 1 || vocab == INT32_MAX || d > INT32_MAX - 1024) return false;
@@ -776,7 +791,18 @@ static bool embed_plan(const dlm_layout_t* L, int32_t vocab, int32_t d, EmbPlan*
     p->off_sid = align_up(p->off_order + size_t(L->n_tokens) * 4, kWsAlign);
     p->off_part = align_up(p->off_sid + size_t(L->n_tokens) * 4, kWsAlign);
     p->bytes = align_up(p->off_part + size_t(p->chunks) * 2 * size_t(p->pitch) * 4, kWsAlign);
-    return true;
+    const int nv = (d + 7) / 8;
+    p->threads = nv >= kGradThreads ? kGradThreads : unsigned(align_up(size_t(nv), 32));
+    p->tiles = int((unsigned(nv) + p->threads - 1) / p->threads);
+    p->join_tiles = (d + kJoinCols - 1) / kJoinCols;
+    p->join_ctas = p->chunks > 1 ? (p->chunks + 31) / 32 * p->join_tiles : 0;
+    p->small_ctas = (int64_t(vocab) + 31) / 32 * ((d + 255) / 256);
+    // half of the table's zeros are written beside the sums, half beside the joins:
+    // both wait on memory more than they use it
+    p->zero_split = p->join_ctas == 0 ? vocab : vocab / 2;
+    // blocks that a launch can have, with the zeros of the wider type
+    const EmbZeros z = embed_zeros(*p, vocab, int64_t(d) * 4);
+    return p->chunks * p->tiles + z.grad <= INT32_MAX && p->join_ctas + z.join <= INT32_MAX && p->small_ctas <= INT32_MAX;
 }
 
 }  // namespace dlm
@@ -823,22 +849,8 @@ extern "C" dlm_status_t dlm_embed_bwd(const dlm_layout_t* layout, const int32_t*
     if (workspace_bytes < p.bytes) return DLM_ERR_WORKSPACE_TOO_SMALL;
     const bool f32 = grad_dtype == DLM_F32;
     const bool vec = d_model % 8 == 0 && ld % 8 == 0 && ld_dw % 8 == 0 && aligned16(d_out) && aligned16(d_weight);
-    const int nv = (d_model + 7) / 8;
-    const unsigned threads = nv >= kGradThreads ? kGradThreads : unsigned(align_up(size_t(nv), 32));
-    const int tiles = int((unsigned(nv) + threads - 1) / threads);
-    const int join_tiles = (d_model + kJoinCols - 1) / kJoinCols;
-    const int64_t join_ctas = p.chunks > 1 ? (p.chunks + 31) / 32 * join_tiles : 0;
-    // half of the table's zeros are written beside the sums, half beside the joins:
-    // both wait on memory more than they use it
-    const int64_t row_bytes = int64_t(d_model) * (f32 ? 4 : 2);
-    const int zero_rows = row_bytes >= kZeroBytes ? 1 : row_bytes * 32 <= kZeroBytes ? 32 : int(kZeroBytes / row_bytes);
-    const int zero_split = join_ctas == 0 ? vocab : vocab / 2;
-    const int64_t per_grad = zero_rows * int64_t(threads / 32), per_join = zero_rows * int64_t(kJoinWarps);
-    const int64_t zero_grad = accumulate ? 0 : (zero_split + per_grad - 1) / per_grad;
-    const int64_t zero_join = accumulate ? 0 : (vocab - zero_split + per_join - 1) / per_join;
-    const int64_t small_ctas = (int64_t(vocab) + 31) / 32 * ((d_model + 255) / 256);
-    if (p.chunks * tiles + zero_grad > INT32_MAX || join_ctas + zero_join > INT32_MAX || small_ctas > INT32_MAX)
-        return DLM_ERR_INVALID_ARGUMENT;
+    const EmbZeros zeros = embed_zeros(p, vocab, int64_t(d_model) * (f32 ? 4 : 2));
+    const int64_t zero_grad = accumulate ? 0 : zeros.grad, zero_join = accumulate ? 0 : zeros.join;
     dlm_status_t st = check_device();
     if (st != DLM_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
@@ -853,7 +865,7 @@ extern "C" dlm_status_t dlm_embed_bwd(const dlm_layout_t* layout, const int32_t*
                           d_weight, ld_dw, hdr, (d_model + 255) / 256, int(aligned16(ids))};
         auto kern = f32 ? (vec ? k_embed_small<8, float> : k_embed_small<1, float>)
                         : (vec ? k_embed_small<8, uint16_t> : k_embed_small<1, uint16_t>);
-        return launch_pdl(kern, dim3(unsigned(small_ctas)), dim3(kSmallWarps * 32), 0, s, "k_embed_small launch", b);
+        return launch_pdl(kern, dim3(unsigned(p.small_ctas)), dim3(kSmallWarps * 32), 0, s, "k_embed_small launch", b);
     }
     // a range of vocabulary rows per SM, as far as the counters fit
     int range = int(align_up(size_t((vocab + 147) / 148), 32));
@@ -869,18 +881,18 @@ extern "C" dlm_status_t dlm_embed_bwd(const dlm_layout_t* layout, const int32_t*
     a.d_out = d_out; a.ld = ld; a.vocab = vocab; a.d = d_model; a.scale = scale; a.accumulate = accumulate;
     a.d_weight = d_weight; a.ld_dw = ld_dw; a.row_start = row_start; a.order = order; a.sid = sid;
     a.part = reinterpret_cast<float*>(ws + p.off_part);
-    a.pitch = p.pitch; a.chunk = p.chunk; a.tiles = tiles; a.n_tokens = layout->n_tokens; a.chunk_ctas = p.chunks * tiles;
-    a.join_ctas = join_ctas; a.join_tiles = join_tiles; a.zero_rows = zero_rows; a.zero_split = zero_split;
+    a.pitch = p.pitch; a.chunk = p.chunk; a.tiles = p.tiles; a.n_tokens = layout->n_tokens; a.chunk_ctas = p.chunks * p.tiles;
+    a.join_ctas = p.join_ctas; a.join_tiles = p.join_tiles; a.zero_rows = zeros.rows; a.zero_split = p.zero_split;
     if (a.chunk_ctas + zero_grad > 0) {
         auto kern = f32 ? (vec ? (accumulate ? k_embed_grad<true, true, float> : k_embed_grad<true, false, float>)
                                : (accumulate ? k_embed_grad<false, true, float> : k_embed_grad<false, false, float>))
                         : (vec ? (accumulate ? k_embed_grad<true, true, uint16_t> : k_embed_grad<true, false, uint16_t>)
                                : (accumulate ? k_embed_grad<false, true, uint16_t> : k_embed_grad<false, false, uint16_t>));
-        st = launch_pdl(kern, dim3(unsigned(a.chunk_ctas + zero_grad)), dim3(threads), vec ? 0 : threads * 8 * sizeof(float),
+        st = launch_pdl(kern, dim3(unsigned(a.chunk_ctas + zero_grad)), dim3(p.threads), vec ? 0 : p.threads * 8 * sizeof(float),
                         s, "k_embed_grad launch", a);
         if (st != DLM_OK) return st;
     }
-    if (join_ctas == 0) return DLM_OK;
-    return launch_pdl(f32 ? k_embed_join<float> : k_embed_join<uint16_t>, dim3(unsigned(join_ctas + zero_join)),
+    if (p.join_ctas == 0) return DLM_OK;
+    return launch_pdl(f32 ? k_embed_join<float> : k_embed_join<uint16_t>, dim3(unsigned(p.join_ctas + zero_join)),
                       dim3(kJoinWarps * 32), 0, s, "k_embed_join launch", a);
 }

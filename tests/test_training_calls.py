@@ -1,6 +1,8 @@
 """What the binding of the embedding, norm and 8-bit calls hands to the library
 and returns to its caller, without a GPU: the library call is replaced by a
 recorder, the rest runs as it is."""
+import ctypes
+
 import pytest
 import torch
 
@@ -197,3 +199,23 @@ def test_no_rows_to_accumulate_launch_nothing():
         assert bwd(0, 4096, None) == 4                     # zeros are written: a launch
     finally:
         assert L.dlm_test_skip_device_check(0) == 0
+
+
+def test_sizes_past_a_launch_s_blocks_have_no_workspace():
+    """A workspace size of 0 for what the call would refuse, whatever the
+    gradient's type and the accumulate option."""
+    dlm_build.build()
+    L = dlm.lib()
+
+    def both(tokens, d, vocab):
+        lay = ctypes.byref(dlm.Layout(1, 0, tokens, 16, None))
+        codes = {L.dlm_embed_bwd(lay, 16, 16, d, vocab, d, 1.0, gt, acc, 16, d, 256, 2 ** 62, None)
+                 for gt in (0, 1) for acc in (0, 1)}
+        return L.dlm_embed_bwd_workspace_size(lay, d, vocab), codes
+    for tokens, d, vocab in ((2 ** 31 - 1, 10 ** 6, 100), (1, 10 ** 6, 2 ** 31 - 2), (2 ** 31 - 1, 2 ** 17, 2 ** 20),
+                             (100, 9000, 2 ** 31 - 2)):
+        assert both(tokens, d, vocab) == (0, {1}), (tokens, d, vocab)
+    if not _a_device_may_be_usable():
+        for tokens, d, vocab in ((2 ** 31 - 1, 16, 100), (2 ** 20, 10 ** 6, 100), (100, 64, 2 ** 31 - 2)):
+            size, codes = both(tokens, d, vocab)
+            assert size > 0 and 1 not in codes and 3 not in codes, (tokens, d, vocab)
