@@ -868,7 +868,7 @@ extern "C" dlm_status_t dlm_embed_bwd(const dlm_layout_t* layout, const int32_t*
         return launch_pdl(kern, dim3(unsigned(p.small_ctas)), dim3(kSmallWarps * 32), 0, s, "k_embed_small launch", b);
     }
     // a range of vocabulary rows per SM, as far as the counters fit
-    int range = int(align_up(size_t((vocab + 147) / 148), 32));
+    int range = int(align_up((size_t(vocab) + 147) / 148, 32));
     if (range > kMaxRange) range = kMaxRange;
     const int warps = range <= kMaxRange / 2 ? 32 : 16;
     if ((st = allow_smem<k_embed_sort, int(kSortSmem)>("k_embed_sort attributes")) != DLM_OK) return st;

@@ -81,3 +81,19 @@ def test_evaluation_allocates_no_8_bit_form():
         bare, z = peak()
     assert torch.equal(y, z) and not z.requires_grad
     assert kept - bare >= x.numel() and bare < x.numel() * 2 + (1 << 20)
+
+
+def test_a_table_of_almost_two_to_the_31_rows():
+    """The most rows that the gradient takes."""
+    V = 2 ** 31 - 2
+    ids = torch.tensor([0, V - 1, 5, V - 1, 2 ** 30, V - 2], dtype=torch.int32, device="cuda")
+    lay = dlm.make_layout(1, 6)
+    dy = torch.tensor([1, 2, 3, 4, 5, 6], device="cuda").to(bf16)[:, None]
+    w = torch.full((V, 1), 9.0, dtype=bf16, device="cuda")
+    out = dlm.embed_bwd(lay, ids, dy, V, d_weight=w)
+    assert out.device_status() == 0 and int(torch.count_nonzero(w)) == 5
+    rows = torch.tensor([0, V - 1, 5, 2 ** 30, V - 2], device="cuda")
+    assert w[rows, 0].tolist() == [1, 6, 3, 5, 6]
+    assert dlm.embed_fwd(lay, ids, w)[:, 0].tolist() == [1, 6, 3, 6, 5, 6]
+    dlm.embed_bwd(lay, ids, dy, V, d_weight=w, accumulate=True, workspace=out.workspace)
+    assert w[rows, 0].tolist() == [2, 12, 6, 10, 12] and int(torch.count_nonzero(w)) == 5
