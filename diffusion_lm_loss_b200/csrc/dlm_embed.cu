@@ -13,7 +13,7 @@
 //                  tokens in row order at the right place (the ids below the
 //                  range, counted in the same pass, give the offset): no
 //                  communication between CTAs, and an order that depends on
-//                  the ids alone.
+//                  the ids and pads, not on timing.
 //   k_embed_grad   one CTA per 8 to 32 sorted positions and column tile adds
 //                  rows in that order, in fp32 registers; a row that begins
 //                  and ends inside the chunk is written at once, a row that

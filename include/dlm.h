@@ -550,8 +550,9 @@ DLM_API dlm_status_t dlm_embed_fwd(const dlm_layout_t *layout, const int32_t *id
  * dlm_embed_bwd -- gradient of the embedding table:
  *   d_weight[v, :] = scale * sum of d_out[i, :] over the tokens i that are no
  *                    pads with ids[i] = v
- * summed in fp32 in an order that depends on the ids alone, and rounded once:
- * results are bitwise reproducible.
+ * summed in fp32 in an order that depends on the ids, the pads and the call's
+ * sizes and types, never on timing, and rounded once: results are bitwise
+ * reproducible.
  *   d_out [n_tokens, ld] bf16; d_weight [vocab, ld_dw] bf16 or float
  *   (grad_dtype DLM_BF16 / DLM_F32).
  *   accumulate = 0: every row of d_weight is written (zeros where no token
@@ -563,7 +564,7 @@ DLM_API dlm_status_t dlm_embed_fwd(const dlm_layout_t *layout, const int32_t *id
  * nothing and set DLM_DEV_BAD_TOKEN_ID in the status word of the workspace
  * (dlm_get_device_status).
  * workspace: at least dlm_embed_bwd_workspace_size() bytes, 256-byte aligned.
- * Errors: as dlm_embed_fwd; an unknown grad_dtype, accumulate other than 0 or
+ * Errors: as dlm_embed_fwd; vocab = 2^31 - 1, an unknown grad_dtype, accumulate other than 0 or
  * 1, a misaligned workspace, or sizes whose launch would pass 2^31 blocks
  * return DLM_ERR_INVALID_ARGUMENT, a workspace that is too small
  * DLM_ERR_WORKSPACE_TOO_SMALL, before anything is enqueued.
@@ -614,8 +615,9 @@ DLM_API dlm_status_t dlm_unpack8(const uint8_t *q, const float *scale, int64_t r
  * 0, or 1 for weights stored as w - 1.  y [rows, ld_y] bf16; mean, rstd
  * [rows] float (kept for the backward pass).
  * pack_format other than DLM_PACK_NONE: q and q_scale get x in the form of
- * dlm_pack8, in the same pass over x where its rows lie on 16-byte borders
- * and d_model <= 32,768.
+ * dlm_pack8, in the same pass over x where the rows of x and y, weight and bias
+ * lie on 16-byte borders and q on an 8-byte one, and d_model is a multiple of 8
+ * up to 32,768; otherwise in a second pass.
  * Errors: rows < 0 or >= 2^31, d_model < 1, a row stride < d_model, an
  * unknown kind, type or format, eps < 0 or not finite, weight_offset not
  * finite or a null pointer return DLM_ERR_INVALID_ARGUMENT.  rows = 0 is a
